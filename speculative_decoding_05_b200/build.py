@@ -5,6 +5,7 @@ import glob
 import os
 import subprocess
 import sys
+import tempfile
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
@@ -14,13 +15,13 @@ INCLUDE = os.path.join(os.path.dirname(HERE), "include")
 NVCC_FLAGS = [
     "-gencode", "arch=compute_100a,code=sm_100a",
     "-lineinfo", "-O3", "-std=c++17",
-    "-Xcompiler", "-fPIC", "-shared",
+    "-Xcompiler", "-fPIC",
 ]
 
 
 def sources():
     return sorted(glob.glob(os.path.join(CSRC, "*.cu")) + glob.glob(os.path.join(CSRC, "*.cuh"))
-                  + [os.path.join(INCLUDE, "dspark.h")])
+                  + glob.glob(os.path.join(CSRC, "*.h")) + glob.glob(os.path.join(INCLUDE, "*.h")))
 
 
 def stale() -> bool:
@@ -31,17 +32,27 @@ def stale() -> bool:
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
-    """Compile csrc/api.cu (which includes every kernel) into libdspark.so."""
+    """Compile csrc/*.cu (each includes the kernels it launches) into libdspark.so."""
     if not force and not stale():
         return LIB
     nvcc = os.environ.get("NVCC", "nvcc")
-    tmp = LIB + f".tmp{os.getpid()}"
-    cmd = [nvcc, *NVCC_FLAGS, "-o", tmp, os.path.join(CSRC, "api.cu")]
-    if verbose:
-        cmd.insert(1, "-Xptxas=-v")
-        print(" ".join(cmd), file=sys.stderr)
-    subprocess.run(cmd, check=True)
-    os.replace(tmp, LIB)
+    with tempfile.TemporaryDirectory(prefix="dspark_build") as tmp:
+        jobs, objs = [], []
+        for cu in sorted(glob.glob(os.path.join(CSRC, "*.cu"))):
+            obj = os.path.join(tmp, os.path.basename(cu) + ".o")
+            cmd = [nvcc, *NVCC_FLAGS, "-c", "-o", obj, cu]
+            if verbose:
+                cmd.insert(1, "-Xptxas=-v")
+                print(" ".join(cmd), file=sys.stderr)
+            jobs.append((cmd, subprocess.Popen(cmd)))
+            objs.append(obj)
+        codes = [j.wait() for _, j in jobs]
+        for (cmd, _), code in zip(jobs, codes):
+            if code != 0:
+                raise subprocess.CalledProcessError(code, cmd)
+        out = LIB + f".tmp{os.getpid()}"
+        subprocess.run([nvcc, *NVCC_FLAGS, "-shared", "-o", out, *objs], check=True)
+        os.replace(out, LIB)
     return LIB
 
 

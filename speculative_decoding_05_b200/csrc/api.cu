@@ -6,8 +6,10 @@
 #include <cstdint>
 #include <cstring>
 #include <mutex>
+#include <vector>
 
 #include "common.cuh"
+#include "kv_status.h"
 #include "prefix.cuh"
 #include "proj_simt.cuh"
 #include "proj_tc.cuh"
@@ -728,10 +730,21 @@ dspark_status dspark_sts_fit(const float* z, const int32_t* n_accepted, long lon
 int dspark_get_device_flags(const void* workspace, void* stream) {
   if (!workspace) return -1;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  unsigned h = 0;
-  if (cudaMemcpyAsync(&h, workspace, sizeof h, cudaMemcpyDeviceToHost, s) != cudaSuccess) return -1;
+  unsigned h[kSpreadHeadWords] = {};
+  if (cudaMemcpyAsync(h, workspace, sizeof h, cudaMemcpyDeviceToHost, s) != cudaSuccess) return -1;
   if (cudaStreamSynchronize(s) != cudaSuccess) return -1;
-  return (int)(h & 0x7fffffffu);  // -1 stays reserved for CUDA errors
+  unsigned n = 0, f = h[0];
+  if (spread_status(h, &n)) {  // a word for each CTA of the call's first kernel
+    std::vector<unsigned> words(n);
+    const unsigned* first = static_cast<const unsigned*>(workspace) + kSpreadHeadWords;
+    if (cudaMemcpyAsync(words.data(), first, n * sizeof(unsigned), cudaMemcpyDeviceToHost, s) !=
+            cudaSuccess ||
+        cudaStreamSynchronize(s) != cudaSuccess)
+      return -1;
+    f = 0;
+    for (const unsigned w : words) f |= w;
+  }
+  return (int)(f & 0x7fffffffu);  // -1 stays reserved for CUDA errors
 }
 
 dspark_status dspark_get_device_status(const void* workspace, void* stream) {

@@ -1,0 +1,129 @@
+// attn_rows.cuh -- attention of single rows, one warp a row: the plain
+// statement of dspark_attn_verify, which touches no key that the row does not
+// see.
+#pragma once
+
+#include "kv_common.cuh"
+
+namespace dspark {
+
+struct AttnArgs {
+  KvRows rows;
+  const void* q;
+  long long q_stride;
+  const void *k_cache, *v_cache;
+  const float *k_scale, *v_scale;
+  void* out;
+  unsigned* status;
+  float scale2;  // sm_scale * log2(e): weights are powers of two of scaled scores
+  int Hq, Hkv, G, window;
+};
+
+// Position range that the row at position i sees.
+__device__ __forceinline__ int first_seen(int i, int window) {
+  return window > 0 && i - window + 1 > 0 ? i - window + 1 : 0;
+}
+
+// One row (request b, position pos, query head hq, `row` of the row tensors)
+// by the 32 lanes of a warp, D / 32 elements a lane; running maximum and sum
+// in fp32.
+template <typename T, typename TC, int D>
+__device__ __noinline__ void attend_row(const AttnArgs& a, int b, int pos, int hq, long long row,
+                                        unsigned& flags) {
+  constexpr int E = D / 32;
+  const KvRows& r = a.rows;
+  const int lane = threadIdx.x & 31;
+  const int h = hq / a.G;
+  float q[E], o[E];
+  const T* qp = static_cast<const T*>(a.q) + row * a.q_stride + (size_t)hq * D + lane * E;
+#pragma unroll
+  for (int e = 0; e < E; e += 2) {
+    const float2 x = Pair<T>::get(*reinterpret_cast<const uint32_t*>(qp + e));
+    q[e] = x.x; q[e + 1] = x.y;
+    o[e] = o[e + 1] = 0.0f;
+  }
+  float m = -CUDART_INF_F, sum = 0.0f;
+  int page = 0;
+  const int mask = (1 << r.page_shift) - 1;
+  const int j0 = first_seen(pos, a.window);
+  for (int j = j0; j <= pos; ++j) {
+    if (j == j0 || (j & mask) == 0) {
+      page = checked_page(r, b, j >> r.page_shift, flags);
+      if (page < 0) page = 0;
+    }
+    const size_t place = ((((size_t)page * a.Hkv + h) << r.page_shift) + (j & mask));
+    float kv[2][E], ks = 1.0f, vs = 1.0f;
+    if constexpr (sizeof(TC) == 1) {
+      ks = a.k_scale[place];
+      vs = a.v_scale[place];
+    }
+#pragma unroll
+    for (int w = 0; w < 2; ++w) {
+      const TC* src = static_cast<const TC*>(w ? a.v_cache : a.k_cache) + place * D + lane * E;
+#pragma unroll
+      for (int e = 0; e < E; e += 2) {
+        float2 x;
+        if constexpr (sizeof(TC) == 1)
+          x = __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2(
+              *reinterpret_cast<const __nv_fp8x2_storage_t*>(src + e), __NV_E4M3)));
+        else
+          x = Pair<T>::get(*reinterpret_cast<const uint32_t*>(src + e));
+        kv[w][e] = x.x; kv[w][e + 1] = x.y;
+      }
+    }
+    float s = 0.0f;
+#pragma unroll
+    for (int e = 0; e < E; ++e) s = fmaf(q[e], kv[0][e], s);
+    s = warp_sum(s) * ks * a.scale2;
+    const float mn = fmaxf(m, s);
+    const float back = mn == -CUDART_INF_F ? 1.0f : exp2f(m - mn);
+    const float w = mn == -CUDART_INF_F && s == s ? 0.0f : exp2f(s - mn);
+    m = mn;
+    sum = sum * back + w;
+#pragma unroll
+    for (int e = 0; e < E; ++e) o[e] = fmaf(w, kv[1][e] * vs, o[e] * back);
+  }
+  const float inv = 1.0f / sum;
+  T* dst = static_cast<T*>(a.out) + (row * a.Hq + hq) * D + lane * E;
+#pragma unroll
+  for (int e = 0; e < E; e += 2)
+    *reinterpret_cast<uint32_t*>(dst + e) = Pair<T>::put(o[e] * inv, o[e + 1] * inv);
+}
+
+constexpr int kAttnRowThreads = 128;
+
+template <typename T, typename TC, int D>
+__global__ void __launch_bounds__(kAttnRowThreads) attn_rows_kernel(const AttnArgs a) {
+  extern __shared__ int s_first[];
+  __shared__ int s_warp[kAttnRowThreads / 32];
+  grid_dep_launch();
+  grid_dep_wait();
+  const KvRows& r = a.rows;
+  unsigned flags = 0;
+  scan_requests<kAttnRowThreads>(r.B, s_first, s_warp, [&](int b) {
+    return checked_new(r, b, r.cache_len[b], r.row_start[b], flags);
+  });
+  const long long total = (long long)s_first[r.B] * a.Hq;
+  for (long long w = (long long)blockIdx.x * (kAttnRowThreads / 32) + threadIdx.x / 32; w < total;
+       w += (long long)gridDim.x * (kAttnRowThreads / 32)) {
+    const int i = (int)(w / a.Hq), hq = (int)(w % a.Hq);
+    const int b = find_request(s_first, r.B, i);
+    const int p = i - s_first[b];
+    const int past = r.cache_len[b];
+    const long long start = r.row_start[b];
+    unsigned again = 0;
+    if (p < 0 || p >= checked_new(r, b, past, start, again)) continue;
+    attend_row<T, TC, D>(a, b, past + p, hq, start + p, flags);
+  }
+  flags = __reduce_or_sync(0xffffffffu, flags);
+  __syncthreads();
+  if ((threadIdx.x & 31) == 0) s_warp[threadIdx.x >> 5] = (int)flags;
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    unsigned f = 0;
+    for (int k = 0; k < kAttnRowThreads / 32; ++k) f |= (unsigned)s_warp[k];
+    store_status(a.status, f);
+  }
+}
+
+}  // namespace dspark

@@ -1,0 +1,301 @@
+// kv.cu -- the C ABI of include/dspark_kv.h: argument validation and launches
+// of the paged-cache calls.
+#include <cuda_runtime.h>
+
+#include <cmath>
+#include <cstdint>
+
+#include "attn_rows.cuh"
+#include "kv_common.cuh"
+#include "kv_rows.cuh"
+#include "kv_status.h"
+
+using namespace dspark;
+
+namespace {
+
+bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
+
+dspark_status launched(cudaError_t e) {
+  // a refused launch also leaves its code behind: take it with it
+  const cudaError_t last = cudaGetLastError();
+  return e == cudaSuccess && last == cudaSuccess ? DSPARK_OK : DSPARK_ERR_CUDA;
+}
+
+int page_shift(int page_size) {
+  for (int s = 4; s <= 8; ++s)
+    if (page_size == 1 << s) return s;
+  return -1;
+}
+
+int kv_sms() {
+  static DeviceOnce once;
+  static int n[kMaxDevices];
+  const int d = current_device();
+  if (d < 0 || d >= kMaxDevices) return 148;
+  once_per_device(once, [&] {
+    int c = 0;
+    if (cudaDeviceGetAttribute(&c, cudaDevAttrMultiProcessorCount, d) != cudaSuccess) c = 0;
+    n[d] = c > 0 ? c : 148;
+  });
+  return n[d];
+}
+
+// Sizes and pointers every call has.
+struct Common {
+  dspark_kv_dtype act, cache;
+  long long n_rows;
+  int B, Hq, Hkv, D;
+  const int64_t* row_start;
+  const int32_t *verify_len, *cache_len, *page_table;
+  int max_pages;
+  const void *k_cache, *v_cache;
+  const float *k_scale, *v_scale;
+  long long n_pages;
+  int page_size;
+  const void* ws;
+  size_t ws_bytes, ws_need;
+};
+
+dspark_status check_common(const Common& c) {
+  if (c.act != DSPARK_KV_BF16 && c.act != DSPARK_KV_F16) return DSPARK_ERR_INVALID_ARG;
+  if (c.cache != DSPARK_KV_E4M3 && c.cache != c.act) return DSPARK_ERR_INVALID_ARG;
+  if (c.B < 0 || c.n_rows < 0 || c.Hkv <= 0 || c.Hq <= 0 || c.D <= 0 || c.max_pages < 0 ||
+      c.n_pages < 0 || c.page_size <= 0)
+    return DSPARK_ERR_INVALID_ARG;
+  if (c.Hq % c.Hkv != 0) return DSPARK_ERR_INVALID_ARG;
+  if ((c.D != 64 && c.D != 128) || page_shift(c.page_size) < 0 || c.B > kKvMaxB || c.Hq > 1024)
+    return DSPARK_ERR_UNSUPPORTED;
+  if (c.n_rows >= (1ll << 31) || c.n_pages >= (1ll << 31) ||
+      c.n_pages * c.Hkv * c.page_size >= (1ll << 31))
+    return DSPARK_ERR_UNSUPPORTED;
+  if (!c.ws || !aligned(c.ws, 256) || c.ws_bytes < c.ws_need) return DSPARK_ERR_WORKSPACE;
+  return DSPARK_OK;
+}
+
+// Pointers, once there is work (B > 0 and n_rows > 0).
+dspark_status check_pointers(const Common& c) {
+  if (!c.row_start || !c.verify_len || !c.cache_len || !c.page_table || !c.k_cache || !c.v_cache ||
+      c.max_pages == 0 || c.n_pages == 0)
+    return DSPARK_ERR_INVALID_ARG;
+  if (!aligned(c.k_cache, 16) || !aligned(c.v_cache, 16) || !aligned(c.row_start, 8) ||
+      !aligned(c.verify_len, 4) || !aligned(c.cache_len, 4) || !aligned(c.page_table, 4))
+    return DSPARK_ERR_INVALID_ARG;
+  if (c.cache == DSPARK_KV_E4M3 && (!c.k_scale || !c.v_scale || !aligned(c.k_scale, 16) ||
+                                    !aligned(c.v_scale, 16)))
+    return DSPARK_ERR_INVALID_ARG;
+  return DSPARK_OK;
+}
+
+KvRows make_rows(const Common& c, int max_len) {
+  KvRows r;
+  r.row_start = c.row_start;
+  r.verify_len = c.verify_len;
+  r.cache_len = c.cache_len;
+  r.page_table = c.page_table;
+  r.n_rows = c.n_rows;
+  r.max_pos = (long long)c.max_pages * c.page_size;
+  if (r.max_pos > (1ll << 31) - 1) r.max_pos = (1ll << 31) - 1;  // positions are int32
+  r.B = c.B;
+  r.max_len = max_len;
+  r.max_pages = c.max_pages;
+  r.page_shift = page_shift(c.page_size);
+  r.n_pages = (int)c.n_pages;
+  return r;
+}
+
+// Nothing to do: a call still clears the status word.
+dspark_status no_work(void* ws, cudaStream_t s) {
+  return cudaMemsetAsync(ws, 0, 64, s) == cudaSuccess ? DSPARK_OK : DSPARK_ERR_CUDA;
+}
+
+// f<T, TC, D>() for the call's types.
+template <typename F>
+dspark_status dispatch(const Common& c, F&& f) {
+  const bool q8 = c.cache == DSPARK_KV_E4M3;
+  if (c.act == DSPARK_KV_BF16) {
+    using T = __nv_bfloat16;
+    if (c.D == 128) return q8 ? f.template run<T, e4m3, 128>() : f.template run<T, T, 128>();
+    return q8 ? f.template run<T, e4m3, 64>() : f.template run<T, T, 64>();
+  }
+  using T = __half;
+  if (c.D == 128) return q8 ? f.template run<T, e4m3, 128>() : f.template run<T, T, 128>();
+  return q8 ? f.template run<T, e4m3, 64>() : f.template run<T, T, 64>();
+}
+
+int row_grid(long long n_rows) {
+  const long long most = 8ll * kv_sms();
+  const long long g = n_rows < most ? n_rows : most;
+  return (int)(g < kMaxStatusCtas ? g : kMaxStatusCtas);
+}
+
+struct LaunchAppend {
+  AppendArgs a;
+  int grid;
+  cudaStream_t s;
+  template <typename T, typename TC, int D>
+  dspark_status run() {
+    return launched(launch_dependent(kv_append_kernel<T, TC, D>, dim3(grid), dim3(kRowThreads),
+                                     (a.rows.B + 1) * sizeof(int), s, a));
+  }
+};
+
+struct LaunchRead {
+  ReadArgs a;
+  int grid;
+  cudaStream_t s;
+  template <typename T, typename TC, int D>
+  dspark_status run() {
+    return launched(launch_dependent(kv_read_kernel<T, TC, D>, dim3(grid), dim3(kRowThreads),
+                                     (a.rows.B + 1) * sizeof(int), s, a));
+  }
+};
+
+struct LaunchAttn {
+  AttnArgs a;
+  cudaStream_t s;
+  template <typename T, typename TC, int D>
+  dspark_status run() {
+    return launched(launch_dependent(attn_rows_kernel<T, TC, D>, dim3(8 * kv_sms()),
+                                     dim3(kAttnRowThreads), (a.rows.B + 1) * sizeof(int), s, a));
+  }
+};
+
+}  // namespace
+
+namespace dspark {
+
+bool spread_status(const unsigned* head, unsigned* count) {
+  if (!(head[0] & kSpreadBit) || head[2] != kSpreadTag || head[1] == 0 ||
+      head[1] > (unsigned)kMaxStatusCtas)
+    return false;
+  *count = head[1];
+  return true;
+}
+
+}  // namespace dspark
+
+extern "C" {
+
+size_t dspark_kv_workspace_size(void) { return kKvHeaderBytes; }
+
+dspark_status dspark_kv_append(
+    const void* q, const void* k, const void* v, int64_t q_stride, int64_t k_stride,
+    int64_t v_stride, dspark_kv_dtype act_dtype, int64_t n_rows, int B, int Hq, int Hkv, int D,
+    const int64_t* row_start, const int32_t* verify_len, const int32_t* cache_len,
+    const int32_t* page_table, int max_pages, void* k_cache, void* v_cache, float* k_scale,
+    float* v_scale, dspark_kv_dtype cache_dtype, int64_t n_pages, int page_size,
+    const float* q_norm, const float* k_norm, float eps, const double* inv_freq, int rot_dim,
+    int interleaved, float rope_scale, void* q_out, void* workspace, size_t ws_bytes,
+    void* stream) {
+  const Common c = {act_dtype, cache_dtype, n_rows,    B,       Hq,      Hkv,     D,
+                    row_start, verify_len,  cache_len, page_table, max_pages, k_cache, v_cache,
+                    k_scale,   v_scale,     n_pages,   page_size, workspace, ws_bytes,
+                    kKvHeaderBytes};
+  dspark_status st = check_common(c);
+  if (st != DSPARK_OK) return st;
+  if (rot_dim < 0 || rot_dim > D || (rot_dim > 0 && !inv_freq) || !std::isfinite(rope_scale) ||
+      !(eps >= 0.0f) || !std::isfinite(eps))
+    return DSPARK_ERR_INVALID_ARG;
+  if (rot_dim % 16 != 0) return DSPARK_ERR_UNSUPPORTED;
+  if (q_stride < (int64_t)Hq * D || k_stride < (int64_t)Hkv * D || v_stride < (int64_t)Hkv * D)
+    return DSPARK_ERR_INVALID_ARG;
+  if (q_stride % 8 || k_stride % 8 || v_stride % 8) return DSPARK_ERR_UNSUPPORTED;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (B == 0 || n_rows == 0) return no_work(workspace, s);
+  if ((st = check_pointers(c)) != DSPARK_OK) return st;
+  if (!q || !k || !v || !q_out) return DSPARK_ERR_INVALID_ARG;
+  if (!aligned(q, 16) || !aligned(k, 16) || !aligned(v, 16) || !aligned(q_out, 16) ||
+      !aligned(q_norm, 4) || !aligned(k_norm, 4) || !aligned(inv_freq, 8))
+    return DSPARK_ERR_INVALID_ARG;
+  LaunchAppend l;
+  AppendArgs& a = l.a;
+  a.rows = make_rows(c, (int)n_rows);
+  a.q = q; a.k = k; a.v = v;
+  a.q_stride = q_stride; a.k_stride = k_stride; a.v_stride = v_stride;
+  a.k_cache = k_cache; a.v_cache = v_cache;
+  a.k_scale = k_scale; a.v_scale = v_scale;
+  a.q_norm = q_norm; a.k_norm = k_norm;
+  a.inv_freq = inv_freq;
+  a.q_out = q_out;
+  a.status = static_cast<unsigned*>(workspace);
+  a.eps = eps; a.rope_scale = rope_scale;
+  a.Hq = Hq; a.Hkv = Hkv; a.rot = rot_dim; a.interleaved = interleaved != 0;
+  l.grid = row_grid(n_rows);
+  l.s = s;
+  return dispatch(c, l);
+}
+
+dspark_status dspark_kv_read(
+    const void* k_cache, const void* v_cache, const float* k_scale, const float* v_scale,
+    dspark_kv_dtype cache_dtype, int64_t n_pages, int page_size, const int64_t* row_start,
+    const int32_t* verify_len, const int32_t* cache_len, const int32_t* page_table, int max_pages,
+    int64_t n_rows, int B, int Hkv, int D, void* k_out, void* v_out, dspark_kv_dtype out_dtype,
+    void* workspace, size_t ws_bytes, void* stream) {
+  const Common c = {out_dtype, cache_dtype, n_rows,    B,       Hkv,     Hkv,     D,
+                    row_start, verify_len,  cache_len, page_table, max_pages, k_cache, v_cache,
+                    k_scale,   v_scale,     n_pages,   page_size, workspace, ws_bytes,
+                    kKvHeaderBytes};
+  dspark_status st = check_common(c);
+  if (st != DSPARK_OK) return st;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (B == 0 || n_rows == 0) return no_work(workspace, s);
+  if ((st = check_pointers(c)) != DSPARK_OK) return st;
+  if (!k_out || !v_out || !aligned(k_out, 16) || !aligned(v_out, 16))
+    return DSPARK_ERR_INVALID_ARG;
+  LaunchRead l;
+  ReadArgs& a = l.a;
+  a.rows = make_rows(c, (int)n_rows);
+  a.k_cache = k_cache; a.v_cache = v_cache;
+  a.k_scale = k_scale; a.v_scale = v_scale;
+  a.k_out = k_out; a.v_out = v_out;
+  a.status = static_cast<unsigned*>(workspace);
+  a.Hkv = Hkv;
+  l.grid = row_grid(n_rows);
+  l.s = s;
+  return dispatch(c, l);
+}
+
+size_t dspark_attn_workspace_size(int B, int Hq, int Hkv, int D, int max_len) {
+  if (B < 0 || Hq <= 0 || Hkv <= 0 || Hq % Hkv != 0 || D <= 0 || max_len <= 0) return 0;
+  return kKvHeaderBytes;
+}
+
+dspark_status dspark_attn_verify(
+    const void* q, int64_t q_stride, dspark_kv_dtype act_dtype, int64_t n_rows, int B, int Hq,
+    int Hkv, int D, int max_len, const int64_t* row_start, const int32_t* verify_len,
+    const int32_t* cache_len, const int32_t* page_table, int max_pages, const void* k_cache,
+    const void* v_cache, const float* k_scale, const float* v_scale, dspark_kv_dtype cache_dtype,
+    int64_t n_pages, int page_size, float sm_scale, int window, void* out, void* workspace,
+    size_t ws_bytes, void* stream) {
+  if (max_len < 1 || window < 0) return DSPARK_ERR_INVALID_ARG;
+  const Common c = {act_dtype, cache_dtype, n_rows,    B,       Hq,      Hkv,     D,
+                    row_start, verify_len,  cache_len, page_table, max_pages, k_cache, v_cache,
+                    k_scale,   v_scale,     n_pages,   page_size, workspace, ws_bytes,
+                    dspark_attn_workspace_size(B, Hq, Hkv, D, max_len)};
+  dspark_status st = check_common(c);
+  if (st != DSPARK_OK) return st;
+  if (!(sm_scale > 0.0f) || !std::isfinite(sm_scale)) return DSPARK_ERR_INVALID_ARG;
+  if (q_stride < (int64_t)Hq * D) return DSPARK_ERR_INVALID_ARG;
+  if (q_stride % 8) return DSPARK_ERR_UNSUPPORTED;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (B == 0 || n_rows == 0) return no_work(workspace, s);
+  if ((st = check_pointers(c)) != DSPARK_OK) return st;
+  if (!q || !out || !aligned(q, 16) || !aligned(out, 16)) return DSPARK_ERR_INVALID_ARG;
+  LaunchAttn l;
+  AttnArgs& a = l.a;
+  a.rows = make_rows(c, max_len);
+  a.q = q;
+  a.q_stride = q_stride;
+  a.k_cache = k_cache; a.v_cache = v_cache;
+  a.k_scale = k_scale; a.v_scale = v_scale;
+  a.out = out;
+  a.status = static_cast<unsigned*>(workspace);
+  a.scale2 = sm_scale * kLog2e;
+  a.Hq = Hq; a.Hkv = Hkv; a.G = Hq / Hkv;
+  a.window = window;
+  l.s = s;
+  return dispatch(c, l);
+}
+
+}  // extern "C"

@@ -1,4 +1,5 @@
-"""Thin Python binding of the C ABI in include/dspark.h (ctypes).
+"""Thin Python binding of the C ABI in include/dspark.h and include/dspark_kv.h
+(ctypes).
 
 Argument marshalling only: tensors are turned into device pointers and
 sizes, every step of the hot path runs in libdspark.so.  The functions carry
@@ -28,8 +29,14 @@ FLAG_NONFINITE = 0x04
 FLAG_BAD_TEMP = 0x08
 FLAG_TIMEOUT = 0x10
 FLAG_BAD_TABLE = 0x20
+FLAG_BAD_PAGE = 0x40
 
-# every symbol include/dspark.h declares
+# element types of the paged-cache calls
+DSPARK_KV_BF16 = 1
+DSPARK_KV_F16 = 2
+DSPARK_KV_E4M3 = 3
+
+# every symbol the headers declare
 SYMBOLS = [
     "dspark_draft_workspace_size", "dspark_draft_markov",
     "dspark_prefix_workspace_size", "dspark_confidence_prefix",
@@ -47,6 +54,11 @@ SYMBOLS = [
     "dspark_sts_workspace_size",
     "dspark_sts_fit",
     "dspark_confidence_prefix_async",
+    "dspark_kv_workspace_size",
+    "dspark_kv_append",
+    "dspark_kv_read",
+    "dspark_attn_workspace_size",
+    "dspark_attn_verify",
 ]
 
 
@@ -121,6 +133,20 @@ def load(path: str | None = None) -> ctypes.CDLL:
     lib.dspark_prefix_path.restype = ctypes.c_char_p
     lib.dspark_version.argtypes = []
     lib.dspark_version.restype = I
+    F = ctypes.c_float
+    lib.dspark_kv_workspace_size.argtypes = []
+    lib.dspark_kv_workspace_size.restype = S
+    lib.dspark_kv_append.argtypes = [P, P, P, L, L, L, I, L, I, I, I, I, P, P, P, P, I, P, P, P, P,
+                                     I, L, I, P, P, F, P, I, I, F, P, P, S, P]
+    lib.dspark_kv_append.restype = I
+    lib.dspark_kv_read.argtypes = [P, P, P, P, I, L, I, P, P, P, P, I, L, I, I, I, P, P, I, P, S,
+                                   P]
+    lib.dspark_kv_read.restype = I
+    lib.dspark_attn_workspace_size.argtypes = [I, I, I, I, I]
+    lib.dspark_attn_workspace_size.restype = S
+    lib.dspark_attn_verify.argtypes = [P, L, I, L, I, I, I, I, I, P, P, P, P, I, P, P, P, P, I, L,
+                                       I, F, I, P, P, S, P]
+    lib.dspark_attn_verify.restype = I
     if path is None:
         _lib = lib
     return lib
@@ -342,3 +368,155 @@ def dspark_confidence_prefix_async(z, temps, cost_tokens, cost_ms, enable, c, su
         _ptr(c), _ptr(survival), _ptr(verify_len), _ptr(objective), _ptr(budget_out),
         _ptr(workspace), workspace.numel(), _stream(stream))
     _check("dspark_confidence_prefix_async", rc)
+
+
+# --------------------------------------------------------------------------
+# the paged cache and its attention (include/dspark_kv.h)
+# --------------------------------------------------------------------------
+
+_KV_TYPES = {torch.bfloat16: DSPARK_KV_BF16, torch.float16: DSPARK_KV_F16,
+             torch.float8_e4m3fn: DSPARK_KV_E4M3}
+
+
+def _at(t):
+    return None if t is None else t.data_ptr()
+
+
+def _kv_type(t, what):
+    code = _KV_TYPES.get(t.dtype)
+    if code is None:
+        raise ValueError(f"{what}: {t.dtype} is not one of bfloat16, float16, float8_e4m3fn")
+    return code
+
+
+def _kv_want(what, t, shape, dtype, device):
+    if tuple(t.shape) != shape or t.dtype != dtype or t.device != device or not t.is_contiguous():
+        raise ValueError(f"{what}: want a contiguous {dtype} tensor of shape {shape} on {device}, "
+                         f"got {t.dtype} {tuple(t.shape)} with strides {t.stride()} on {t.device}")
+
+
+def _kv_rows(what, t, n_rows, D, device, dtype):
+    """A row tensor [n_rows, H, D] whose rows may be apart: (H, row stride)."""
+    if (t.dim() != 3 or t.shape[0] != n_rows or t.shape[2] != D or t.dtype != dtype
+            or t.device != device or (t.shape[1] * D > 0 and n_rows > 0
+                                      and (t.stride(2) != 1 or t.stride(1) != D))):
+        raise ValueError(f"{what}: want {dtype} rows [{n_rows}, heads, {D}] with contiguous heads "
+                         f"on {device}, got {t.dtype} {tuple(t.shape)} with strides {t.stride()} "
+                         f"on {t.device}")
+    H = t.shape[1]
+    return H, (t.stride(0) if n_rows > 1 else H * D)
+
+
+def _kv_cache(k_cache, v_cache, k_scale, v_scale, row_start, verify_len, cache_len, page_table):
+    """Checks of what the three calls share; returns (cache code, n_pages,
+    Hkv, page_size, D, B, max_pages, device)."""
+    if k_cache.dim() != 4:
+        raise ValueError(f"k_cache: want [n_pages, Hkv, page_size, D], got {tuple(k_cache.shape)}")
+    code = _kv_type(k_cache, "k_cache")
+    dev = k_cache.device
+    shape = tuple(k_cache.shape)
+    _kv_want("k_cache", k_cache, shape, k_cache.dtype, dev)
+    _kv_want("v_cache", v_cache, shape, k_cache.dtype, dev)
+    if code == DSPARK_KV_E4M3:
+        if k_scale is None or v_scale is None:
+            raise ValueError("an e4m3 cache needs k_scale and v_scale")
+        _kv_want("k_scale", k_scale, shape[:3], torch.float32, dev)
+        _kv_want("v_scale", v_scale, shape[:3], torch.float32, dev)
+    elif k_scale is not None or v_scale is not None:
+        raise ValueError("k_scale and v_scale belong to an e4m3 cache")
+    if page_table.dim() != 2:
+        raise ValueError(f"page_table: want [B, max_pages], got {tuple(page_table.shape)}")
+    B, max_pages = page_table.shape
+    _kv_want("page_table", page_table, (B, max_pages), torch.int32, dev)
+    _kv_want("row_start", row_start, (B,), torch.int64, dev)
+    _kv_want("verify_len", verify_len, (B,), torch.int32, dev)
+    _kv_want("cache_len", cache_len, (B,), torch.int32, dev)
+    return (code, *shape, B, max_pages, dev)
+
+
+def _kv_call(name, device, workspace, stream, args):
+    """Calls the library with the tensors' device current, on `stream` or
+    that device's current stream."""
+    if workspace.device != device:
+        raise ValueError(f"{name}: the workspace is on {workspace.device}, the tensors on {device}")
+    fn = getattr(load(), name)
+    ws, n = workspace.data_ptr(), workspace.numel() * workspace.element_size()
+    if device.type != "cuda":  # refused calls come back before any launch
+        rc = fn(*args, ws, n, stream.cuda_stream if stream is not None else 0)
+    else:
+        with torch.cuda.device(device):
+            s = stream if stream is not None else torch.cuda.current_stream()
+            rc = fn(*args, ws, n, s.cuda_stream)
+    _check(name, rc)
+
+
+def dspark_kv_workspace_size() -> int:
+    return int(load().dspark_kv_workspace_size())
+
+
+def dspark_kv_append(q, k, v, row_start, verify_len, cache_len, page_table, k_cache, v_cache,
+                     q_out, workspace, k_scale=None, v_scale=None, q_norm=None, k_norm=None,
+                     eps=1e-6, inv_freq=None, interleaved=False, rope_scale=1.0, stream=None):
+    """Norms and rotation of the new rows' queries and keys, keys and values
+    written to the paged cache.  q [n_rows, Hq, D], k, v [n_rows, Hkv, D] (row
+    strides free), inv_freq [rot_dim / 2] fp64 (None: no rotation)."""
+    code, n_pages, Hkv, ps, D, B, max_pages, dev = _kv_cache(
+        k_cache, v_cache, k_scale, v_scale, row_start, verify_len, cache_len, page_table)
+    act = _kv_type(q, "q")
+    n_rows = q.shape[0]
+    Hq, qs = _kv_rows("q", q, n_rows, D, dev, q.dtype)
+    Hk, ks = _kv_rows("k", k, n_rows, D, dev, q.dtype)
+    Hv, vs = _kv_rows("v", v, n_rows, D, dev, q.dtype)
+    if Hk != Hkv or Hv != Hkv:
+        raise ValueError(f"k and v have {Hk} and {Hv} heads, the cache {Hkv}")
+    _kv_want("q_out", q_out, (n_rows, Hq, D), q.dtype, dev)
+    for what, w in (("q_norm", q_norm), ("k_norm", k_norm)):
+        if w is not None:
+            _kv_want(what, w, (D,), torch.float32, dev)
+    rot = 0
+    if inv_freq is not None:
+        rot = 2 * inv_freq.numel()
+        _kv_want("inv_freq", inv_freq, (rot // 2,), torch.float64, dev)
+    _kv_call("dspark_kv_append", dev, workspace, stream,
+             (_at(q), _at(k), _at(v), qs, ks, vs, act, n_rows, B, Hq, Hkv, D, _at(row_start),
+              _at(verify_len), _at(cache_len), _at(page_table), max_pages, _at(k_cache),
+              _at(v_cache), _at(k_scale), _at(v_scale), code, n_pages, ps, _at(q_norm),
+              _at(k_norm), eps, _at(inv_freq), rot, int(bool(interleaved)), rope_scale,
+              _at(q_out)))
+
+
+def dspark_kv_read(k_cache, v_cache, row_start, verify_len, cache_len, page_table, k_out, v_out,
+                   workspace, k_scale=None, v_scale=None, stream=None):
+    """Rows of the paged cache (dequantised) into k_out, v_out
+    [n_rows, Hkv, D]: positions cache_len[b] + p, p = 0 .. verify_len[b]."""
+    code, n_pages, Hkv, ps, D, B, max_pages, dev = _kv_cache(
+        k_cache, v_cache, k_scale, v_scale, row_start, verify_len, cache_len, page_table)
+    n_rows = k_out.shape[0]
+    _kv_want("k_out", k_out, (n_rows, Hkv, D), k_out.dtype, dev)
+    _kv_want("v_out", v_out, (n_rows, Hkv, D), k_out.dtype, dev)
+    _kv_call("dspark_kv_read", dev, workspace, stream,
+             (_at(k_cache), _at(v_cache), _at(k_scale), _at(v_scale), code, n_pages, ps,
+              _at(row_start), _at(verify_len), _at(cache_len), _at(page_table), max_pages, n_rows,
+              B, Hkv, D, _at(k_out), _at(v_out), _kv_type(k_out, "k_out")))
+
+
+def dspark_attn_workspace_size(B, Hq, Hkv, D, max_len) -> int:
+    return int(load().dspark_attn_workspace_size(B, Hq, Hkv, D, max_len))
+
+
+def dspark_attn_verify(q, k_cache, v_cache, row_start, verify_len, cache_len, page_table, out,
+                       workspace, max_len, k_scale=None, v_scale=None, sm_scale=None, window=0,
+                       stream=None):
+    """Causal attention of the new rows q [n_rows, Hq, D] over the paged
+    cache; max_len bounds verify_len + 1; sm_scale None: 1 / sqrt(D)."""
+    code, n_pages, Hkv, ps, D, B, max_pages, dev = _kv_cache(
+        k_cache, v_cache, k_scale, v_scale, row_start, verify_len, cache_len, page_table)
+    n_rows = q.shape[0]
+    act = _kv_type(q, "q")
+    Hq, qs = _kv_rows("q", q, n_rows, D, dev, q.dtype)
+    _kv_want("out", out, (n_rows, Hq, D), q.dtype, dev)
+    _kv_call("dspark_attn_verify", dev, workspace, stream,
+             (_at(q), qs, act, n_rows, B, Hq, Hkv, D, max_len, _at(row_start), _at(verify_len),
+              _at(cache_len), _at(page_table), max_pages, _at(k_cache), _at(v_cache),
+              _at(k_scale), _at(v_scale), code, n_pages, ps,
+              D ** -0.5 if sm_scale is None else sm_scale, window, _at(out)))
