@@ -1,6 +1,6 @@
 // attn_rows.cuh -- attention of single rows, one warp a row: the plain
 // statement of dspark_attn_verify, which touches no key that the row does not
-// see.
+// see.  The tiled kernels fall back to it for rows whose result is not finite.
 #pragma once
 
 #include "kv_common.cuh"
@@ -88,42 +88,6 @@ __device__ __noinline__ void attend_row(const AttnArgs& a, int b, int pos, int h
 #pragma unroll
   for (int e = 0; e < E; e += 2)
     *reinterpret_cast<uint32_t*>(dst + e) = Pair<T>::put(o[e] * inv, o[e + 1] * inv);
-}
-
-constexpr int kAttnRowThreads = 128;
-
-template <typename T, typename TC, int D>
-__global__ void __launch_bounds__(kAttnRowThreads) attn_rows_kernel(const AttnArgs a) {
-  extern __shared__ int s_first[];
-  __shared__ int s_warp[kAttnRowThreads / 32];
-  grid_dep_launch();
-  grid_dep_wait();
-  const KvRows& r = a.rows;
-  unsigned flags = 0;
-  scan_requests<kAttnRowThreads>(r.B, s_first, s_warp, [&](int b) {
-    return checked_new(r, b, r.cache_len[b], r.row_start[b], flags);
-  });
-  const long long total = (long long)s_first[r.B] * a.Hq;
-  for (long long w = (long long)blockIdx.x * (kAttnRowThreads / 32) + threadIdx.x / 32; w < total;
-       w += (long long)gridDim.x * (kAttnRowThreads / 32)) {
-    const int i = (int)(w / a.Hq), hq = (int)(w % a.Hq);
-    const int b = find_request(s_first, r.B, i);
-    const int p = i - s_first[b];
-    const int past = r.cache_len[b];
-    const long long start = r.row_start[b];
-    unsigned again = 0;
-    if (p < 0 || p >= checked_new(r, b, past, start, again)) continue;
-    attend_row<T, TC, D>(a, b, past + p, hq, start + p, flags);
-  }
-  flags = __reduce_or_sync(0xffffffffu, flags);
-  __syncthreads();
-  if ((threadIdx.x & 31) == 0) s_warp[threadIdx.x >> 5] = (int)flags;
-  __syncthreads();
-  if (threadIdx.x == 0) {
-    unsigned f = 0;
-    for (int k = 0; k < kAttnRowThreads / 32; ++k) f |= (unsigned)s_warp[k];
-    store_status(a.status, f);
-  }
 }
 
 }  // namespace dspark

@@ -1,11 +1,14 @@
 // kv.cu -- the C ABI of include/dspark_kv.h: argument validation and launches
 // of the paged-cache calls.
+#include <cuda.h>
+#include <cudaTypedefs.h>
 #include <cuda_runtime.h>
 
 #include <cmath>
 #include <cstdint>
+#include <type_traits>
 
-#include "attn_rows.cuh"
+#include "attn_split.cuh"
 #include "kv_common.cuh"
 #include "kv_rows.cuh"
 #include "kv_status.h"
@@ -17,9 +20,9 @@ namespace {
 bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
 dspark_status launched(cudaError_t e) {
-  // a refused launch also leaves its code behind: take it with it
-  const cudaError_t last = cudaGetLastError();
-  return e == cudaSuccess && last == cudaSuccess ? DSPARK_OK : DSPARK_ERR_CUDA;
+  if (e == cudaSuccess) return DSPARK_OK;
+  cudaGetLastError();  // a refused launch also leaves its code behind
+  return DSPARK_ERR_CUDA;
 }
 
 int page_shift(int page_size) {
@@ -151,19 +154,97 @@ struct LaunchRead {
   }
 };
 
+// CTAs of the attention kernels: the partial results of a workspace have room
+// for two CTAs on each of a B200's SMs.
+constexpr int kAttnMaxSms = 148;
+int attn_sms() { return kv_sms() < kAttnMaxSms ? kv_sms() : kAttnMaxSms; }
+
+constexpr int kSplitMaxRows = 32;
+
 struct LaunchAttn {
   AttnArgs a;
+  long long rows_per_head;  // at most, of one request
+  long long cache_rows;
+  int page_size, D;
+  unsigned char* ws;
   cudaStream_t s;
-  template <typename T, typename TC, int D>
+
+  AttnParts parts(int ctas, int rows) const {
+    const PartBytes b = part_bytes(ctas, rows, D);
+    AttnParts p;
+    p.rec = reinterpret_cast<PartRecord*>(ws + b.rec);
+    p.ml = reinterpret_cast<float2*>(ws + b.ml);
+    p.o = reinterpret_cast<float*>(ws + b.o);
+    return p;
+  }
+
+  template <typename T, typename TC>
+  bool maps(CUtensorMap* mk, CUtensorMap* mv, int keys, int* box) const {
+    constexpr bool f16 = std::is_same<T, __half>::value;
+    *box = page_size < keys ? page_size : keys;
+    return encode_cache_map(mk, a.k_cache, D, sizeof(TC) == 1, f16, cache_rows, *box) &&
+           encode_cache_map(mv, a.v_cache, D, sizeof(TC) == 1, f16, cache_rows, *box);
+  }
+
+  template <typename T, typename TC, int Dh>
+  dspark_status join(const AttnTiles& t, const AttnParts& p, int ctas) const {
+    const int groups = (t.rows * (Dh / 4) + kJoinThreads - 1) / kJoinThreads;
+    return launched(launch_dependent(attn_join_kernel<T, TC, Dh>, dim3(ctas, groups < 4 ? groups : 4),
+                                     dim3(kJoinThreads), 0, s, a, t, p, ctas));
+  }
+
+  template <typename T, typename TC, int Dh, int MT>
+  dspark_status split() const {
+    constexpr int smem = (int)sizeof(SplitSmem<TC, Dh, MT>) + 1024;
+    static DeviceOnce once;
+    set_smem_once(once, attn_split_kernel<T, TC, Dh, MT>, smem);
+    const int ctas = 2 * attn_sms();
+    const AttnTiles t = {16 * MT, split_keys<TC, Dh>()};
+    const AttnParts p = parts(ctas, t.rows);
+    CUtensorMap mk, mv;
+    int box;
+    if (!maps<T, TC>(&mk, &mv, t.keys, &box)) return DSPARK_ERR_CUDA;
+    const dspark_status st = launched(launch_dependent(attn_split_kernel<T, TC, Dh, MT>, dim3(ctas),
+                                                       dim3(kSplitThreads), smem, s, a, p, mk, mv,
+                                                       box));
+    return st != DSPARK_OK ? st : join<T, TC, Dh>(t, p, ctas);
+  }
+
+  template <typename T, typename TC, int Dh>
   dspark_status run() {
-    return launched(launch_dependent(attn_rows_kernel<T, TC, D>, dim3(8 * kv_sms()),
-                                     dim3(kAttnRowThreads), (a.rows.B + 1) * sizeof(int), s, a));
+    return rows_per_head <= 16 ? split<T, TC, Dh, 1>() : split<T, TC, Dh, 2>();
   }
 };
 
 }  // namespace
 
 namespace dspark {
+
+bool encode_cache_map(CUtensorMap* m, const void* cache, int D, bool is_e4m3, bool is_f16,
+                      long long rows, int box_rows) {
+  // the driver's entry point, looked up once
+  static const PFN_cuTensorMapEncodeTiled_v12000 fn = [] {
+    void* p = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &p, cudaEnableDefault, &q) ==
+            cudaSuccess &&
+        q == cudaDriverEntryPointSuccess)
+      return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
+    return (PFN_cuTensorMapEncodeTiled_v12000) nullptr;
+  }();
+  if (!fn) return false;
+  const cuuint64_t dims[2] = {(cuuint64_t)D, (cuuint64_t)rows};
+  const cuuint64_t strides[1] = {(cuuint64_t)D * (is_e4m3 ? 1 : 2)};
+  const cuuint32_t box[2] = {is_e4m3 ? (cuuint32_t)D : 64u, (cuuint32_t)box_rows};
+  const cuuint32_t es[2] = {1, 1};
+  const CUtensorMapDataType type = is_e4m3  ? CU_TENSOR_MAP_DATA_TYPE_UINT8
+                                   : is_f16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16
+                                            : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+  return fn(m, type, 2, const_cast<void*>(cache), dims, strides, box, es,
+            CU_TENSOR_MAP_INTERLEAVE_NONE,
+            is_e4m3 && D == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
 
 bool spread_status(const unsigned* head, unsigned* count) {
   if (!(head[0] & kSpreadBit) || head[2] != kSpreadTag || head[1] == 0 ||
@@ -258,7 +339,7 @@ dspark_status dspark_kv_read(
 
 size_t dspark_attn_workspace_size(int B, int Hq, int Hkv, int D, int max_len) {
   if (B < 0 || Hq <= 0 || Hkv <= 0 || Hq % Hkv != 0 || D <= 0 || max_len <= 0) return 0;
-  return kKvHeaderBytes;
+  return part_bytes(2 * kAttnMaxSms, kSplitMaxRows, D).total;
 }
 
 dspark_status dspark_attn_verify(
@@ -294,6 +375,12 @@ dspark_status dspark_attn_verify(
   a.scale2 = sm_scale * kLog2e;
   a.Hq = Hq; a.Hkv = Hkv; a.G = Hq / Hkv;
   a.window = window;
+  if (n_rows * Hq >= (1ll << 31)) return DSPARK_ERR_UNSUPPORTED;
+  l.rows_per_head = (max_len < n_rows ? max_len : n_rows) * a.G;
+  l.cache_rows = n_pages * Hkv * page_size;
+  l.page_size = page_size;
+  l.D = D;
+  l.ws = static_cast<unsigned char*>(workspace);
   l.s = s;
   return dispatch(c, l);
 }
