@@ -23,6 +23,7 @@
 #include <type_traits>
 
 #include "attn_plan.cuh"
+#include "attn_tc.cuh"
 
 namespace dspark {
 
@@ -82,26 +83,6 @@ __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], 
         "{%8,%9}, {%0,%1,%2,%3};"
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-}
-
-// Two e4m3 codes, in the high bytes of the halves of x (low bytes 0), as 16-bit
-// values: the four exponent bits land on the low exponent bits of the wider
-// type (subnormal codes on its subnormals), and a power of two makes up for
-// the difference of the biases: 2^(127 - 7) for bf16, 2^(15 - 7) for fp16.
-// Both steps are exact.
-template <typename T>
-__device__ __forceinline__ uint32_t widen2(uint32_t x) {
-  if constexpr (__is_same(T, __half)) {
-    const uint32_t y = (x & 0x80008000u) | ((x >> 1) & 0x3f803f80u);
-    const __half2 r = __hmul2(*reinterpret_cast<const __half2*>(&y), __floats2half2_rn(256.0f, 256.0f));
-    return *reinterpret_cast<const uint32_t*>(&r);
-  } else {
-    const uint32_t y = (x & 0x80008000u) | ((x >> 4) & 0x07f007f0u);
-    const uint32_t two120 = 0x7b807b80u;
-    const __nv_bfloat162 r = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&y),
-                                     *reinterpret_cast<const __nv_bfloat162*>(&two120));
-    return *reinterpret_cast<const uint32_t*>(&r);
-  }
 }
 
 template <typename T, typename TC, int D, int MT>

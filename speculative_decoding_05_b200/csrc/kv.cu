@@ -9,6 +9,7 @@
 #include <type_traits>
 
 #include "attn_split.cuh"
+#include "attn_step.cuh"
 #include "kv_common.cuh"
 #include "kv_rows.cuh"
 #include "kv_status.h"
@@ -210,9 +211,29 @@ struct LaunchAttn {
     return st != DSPARK_OK ? st : join<T, TC, Dh>(t, p, ctas);
   }
 
+  template <typename T, typename TC, int Dh, int N>
+  dspark_status step() const {
+    constexpr int smem = (int)sizeof(StepSmem<TC, Dh, N>) + 1024;
+    static_assert(smem <= kSmemLimit, "shared memory");
+    static DeviceOnce once;
+    set_smem_once(once, attn_step_kernel<T, TC, Dh, N>, smem);
+    const int ctas = attn_sms();
+    const AttnTiles t = {N, kStepKeys};
+    const AttnParts p = parts(ctas, t.rows);
+    CUtensorMap mk, mv;
+    int box;
+    if (!maps<T, TC>(&mk, &mv, t.keys, &box)) return DSPARK_ERR_CUDA;
+    const dspark_status st = launched(launch_dependent(attn_step_kernel<T, TC, Dh, N>, dim3(ctas),
+                                                       dim3(step_threads<TC>()), smem, s, a, p, mk,
+                                                       mv, box));
+    return st != DSPARK_OK ? st : join<T, TC, Dh>(t, p, ctas);
+  }
+
   template <typename T, typename TC, int Dh>
   dspark_status run() {
-    return rows_per_head <= 16 ? split<T, TC, Dh, 1>() : split<T, TC, Dh, 2>();
+    if (rows_per_head <= 32) return step<T, TC, Dh, 32>();
+    if (rows_per_head <= 64) return step<T, TC, Dh, 64>();
+    return step<T, TC, Dh, 128>();
   }
 };
 
@@ -339,7 +360,7 @@ dspark_status dspark_kv_read(
 
 size_t dspark_attn_workspace_size(int B, int Hq, int Hkv, int D, int max_len) {
   if (B < 0 || Hq <= 0 || Hkv <= 0 || Hq % Hkv != 0 || D <= 0 || max_len <= 0) return 0;
-  return part_bytes(2 * kAttnMaxSms, kSplitMaxRows, D).total;
+  return part_bytes(kAttnMaxSms, 128, D).total;
 }
 
 dspark_status dspark_attn_verify(
