@@ -21,7 +21,7 @@ namespace dspark {
 
 // What an item costs besides its key tiles, in key tiles: rows loaded,
 // results merged and stored.
-constexpr int kItemCost = 1;
+constexpr int kItemCost = 2;
 // Least cost of a CTA's piece.  Below it a further CTA saves less than the
 // join of its part costs.
 constexpr int kMinPiece = 2;
@@ -32,32 +32,38 @@ struct AttnTiles {
 };
 
 // Key tiles of row tile qt, and the first of them.
-__device__ __forceinline__ int item_tiles(const AttnTiles& t, int G, int window, int n, int past,
+__device__ __forceinline__ int item_tiles(const AttnTiles& t, const AttnArgs& a, int n, int past,
                                           int qt, int& lo) {
-  const int first = qt * t.rows / G;
-  int last = (int)(((long long)(qt + 1) * t.rows - 1) / G);
-  if (last > n - 1) last = n - 1;
-  lo = first_seen(past + first, window) / t.keys;
+  const int first = a.by_g.div(qt * t.rows);
+  const int last = a.by_g.div(min((qt + 1) * t.rows, n * a.G) - 1);
+  lo = first_seen(past + first, a.window) / t.keys;
   return (past + last) / t.keys + 1 - lo;
 }
 __device__ __forceinline__ int row_tiles(const AttnTiles& t, int G, int n) {
   return (n * G + t.rows - 1) / t.rows;
 }
 // Cost of one head of a request.
-__device__ __forceinline__ long long head_cost(const AttnTiles& t, int G, int window, int n,
+__device__ __forceinline__ long long head_cost(const AttnTiles& t, const AttnArgs& a, int n,
                                                int past) {
   long long c = 0;
-  const int nq = row_tiles(t, G, n);
+  const int nq = row_tiles(t, a.G, n);
   for (int qt = 0; qt < nq; ++qt) {
     int lo;
-    c += item_tiles(t, G, window, n, past, qt, lo) + kItemCost;
+    c += item_tiles(t, a, n, past, qt, lo) + kItemCost;
   }
   return c;
 }
+// x / y, by the short way where both fit 32 bits.
+__device__ __forceinline__ long long quotient(long long x, long long y) {
+  if (((x | y) >> 32) == 0) return (unsigned)x / (unsigned)y;
+  return x / y;
+}
 
 struct Piece {
-  long long off, len;  // start behind the start of request b, and length
-  int b;
+  long long len;       // cost
+  long long off;       // start behind the start of its first item
+  long long row0;      // first item: see Item
+  int b, h, qt, n, past;
 };
 
 // This CTA's piece of the line, by the NT threads of the block.
@@ -68,45 +74,68 @@ __device__ __forceinline__ void find_piece(const AttnArgs& a, const AttnTiles& t
   const int per = (r.B + NT - 1) / NT;
   const int b0 = threadIdx.x * per, b1 = min(b0 + per, r.B);
   const int w = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  auto cost = [&](int b) -> long long {
-    const int past = r.cache_len[b];
-    const int n = checked_new(r, b, past, r.row_start[b], flags);
-    return n ? a.Hkv * head_cost(t, a.G, a.window, n, past) : 0;
+  int past = 0, n = 0;
+  long long row0 = 0, head = 0;
+  auto request = [&](int b) {  // the four above, and the request's cost
+    past = r.cache_len[b];
+    row0 = r.row_start[b];
+    n = checked_new(r, b, past, row0, flags);
+    head = n ? head_cost(t, a, n, past) : 0;
+    return a.Hkv * head;
   };
   long long mine = 0;
-  for (int b = b0; b < b1; ++b) mine += cost(b);
+  for (int b = b0; b < b1; ++b) mine += request(b);
   long long incl = mine;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const long long n = __shfl_up_sync(0xffffffffu, incl, o);
-    if (lane >= o) incl += n;
+    const long long v = __shfl_up_sync(0xffffffffu, incl, o);
+    if (lane >= o) incl += v;
   }
   if (lane == 31) s_warp[w] = incl;
   if (threadIdx.x == 0) {
-    s_piece->b = 0;
-    s_piece->len = 0;
-    s_piece->off = 0;
+    s_piece->b = s_piece->h = s_piece->qt = s_piece->n = s_piece->past = 0;
+    s_piece->len = s_piece->off = s_piece->row0 = 0;
   }
   __syncthreads();
   long long pre = incl - mine, total = 0;
+#pragma unroll
   for (int i = 0; i < NT / 32; ++i) {
-    if (i < w) pre += s_warp[i];
-    total += s_warp[i];
+    const long long v = s_warp[i];
+    if (i < w) pre += v;
+    total += v;
   }
   long long ctas = total / kMinPiece;
   if (ctas > gridDim.x) ctas = gridDim.x;
   if (ctas < 1) ctas = 1;
   const long long c = blockIdx.x;
   if (c < ctas) {
-    const long long start = total * c / ctas, end = total * (c + 1) / ctas;
-    if (start >= pre && start < pre + mine && end > start) {
+    // equal pieces, the first total % ctas of them longer by one
+    const long long len = quotient(total, ctas), more = total - len * ctas;
+    const long long start = c * len + min(c, more);
+    const long long mylen = len + (c < more);
+    if (mylen > 0 && start >= pre && start < pre + mine) {
       long long at = pre;
       for (int b = b0; b < b1; ++b) {
-        const long long k = cost(b);
+        const long long k = per == 1 ? mine : request(b);
         if (start < at + k) {
+          long long off = start - at;
+          const int h = (int)quotient(off, head);
+          off -= h * head;
+          int qt = 0, lo;
+          while (true) {
+            const int ic = item_tiles(t, a, n, past, qt, lo) + kItemCost;
+            if (off < ic) break;
+            off -= ic;
+            ++qt;
+          }
           s_piece->b = b;
-          s_piece->off = start - at;
-          s_piece->len = end - start;
+          s_piece->h = h;
+          s_piece->qt = qt;
+          s_piece->n = n;
+          s_piece->past = past;
+          s_piece->row0 = row0;
+          s_piece->off = off;
+          s_piece->len = mylen;
           break;
         }
         at += k;
@@ -152,18 +181,14 @@ struct Walk {
   __device__ __forceinline__ void start(const AttnArgs& a, const AttnTiles& t, const Piece& p) {
     left = p.len;
     open = left > 0;
-    if (!open) return;
-    request(a, t, p.b);
-    const long long per = head_cost(t, a.G, a.window, n, past);
-    h = (int)(p.off / per);
-    off = p.off - h * per;
-    while (true) {
-      int lo;
-      const int c = item_tiles(t, a.G, a.window, n, past, qt, lo) + kItemCost;
-      if (off < c) break;
-      off -= c;
-      ++qt;
-    }
+    off = p.off;
+    b = p.b;
+    h = p.h;
+    qt = p.qt;
+    n = p.n;
+    past = p.past;
+    row0 = p.row0;
+    nq = row_tiles(t, a.G, n);
   }
   // The next item with key tiles in the piece; part = -1 at its end.
   __device__ __forceinline__ Item next(const AttnArgs& a, const AttnTiles& t) {
@@ -171,7 +196,7 @@ struct Walk {
     it.part = -1;
     while (open && left > 0 && b < a.rows.B) {
       int lo;
-      const int nt = item_tiles(t, a.G, a.window, n, past, qt, lo);
+      const int nt = item_tiles(t, a, n, past, qt, lo);
       const long long begin = off, end = min(off + left, (long long)(nt + kItemCost));
       const int t0 = (int)max(begin - kItemCost, 0ll), t1 = (int)max(end - kItemCost, 0ll);
       if (t1 > t0) {
@@ -285,7 +310,7 @@ __global__ void __launch_bounds__(kJoinThreads)
       const float inv = 1.0f / L;
       o.x *= inv; o.y *= inv; o.z *= inv; o.w *= inv;
       if (!isfinite(o.x) || !isfinite(o.y) || !isfinite(o.z) || !isfinite(o.w)) s_bad[rg] = 1;
-      const int rr = rec.qt * t.rows + r, tok = rr / a.G;
+      const int rr = rec.qt * t.rows + r, tok = a.by_g.div(rr);
       T* dst = static_cast<T*>(a.out) +
                ((rec.row0 + tok) * a.Hq + rec.h * a.G + rr - tok * a.G) * D + 4 * lane;
       *reinterpret_cast<uint2*>(dst) = make_uint2(Pair<T>::put(o.x, o.y), Pair<T>::put(o.z, o.w));
@@ -295,7 +320,7 @@ __global__ void __launch_bounds__(kJoinThreads)
     // not see (0 times infinity): form the row again from those it sees
     for (int k = threadIdx.x / 32; k < kRows; k += kJoinThreads / 32) {
       if (!s_bad[k]) continue;
-      const int rr = rec.qt * t.rows + r0 + k, tok = rr / a.G;
+      const int rr = rec.qt * t.rows + r0 + k, tok = a.by_g.div(rr);
       unsigned flags = 0;
       attend_row<T, TC, D>(a, rec.b, rec.past + tok, rec.h * a.G + rr - tok * a.G, rec.row0 + tok,
                            flags);

@@ -7,6 +7,25 @@
 
 namespace dspark {
 
+// Division of 0 <= x < 2^31 by a divisor known on the host: with l = ceil(log2 d)
+// and m = floor(2^(31 + l) / d) + 1, x m / 2^(31 + l) exceeds x / d by less than
+// x / 2^(31 + l) <= 1 / d, so its whole part is the quotient.
+struct Divisor {
+  unsigned m;
+  int shift;
+  __device__ __forceinline__ int div(int x) const {
+    return (int)(((unsigned long long)(unsigned)x * m) >> shift);
+  }
+};
+inline Divisor make_divisor(int d) {
+  int l = 0;
+  while ((1 << l) < d) ++l;
+  Divisor r;
+  r.m = (unsigned)((1ull << (31 + l)) / (unsigned)d + 1);
+  r.shift = 31 + l;
+  return r;
+}
+
 struct AttnArgs {
   KvRows rows;
   const void* q;
@@ -17,6 +36,7 @@ struct AttnArgs {
   unsigned* status;
   float scale2;  // sm_scale * log2(e): weights are powers of two of scaled scores
   int Hq, Hkv, G, window;
+  Divisor by_g;  // by G
 };
 
 // Position range that the row at position i sees.
@@ -33,7 +53,7 @@ __device__ __noinline__ void attend_row(const AttnArgs& a, int b, int pos, int h
   constexpr int E = D / 32;
   const KvRows& r = a.rows;
   const int lane = threadIdx.x & 31;
-  const int h = hq / a.G;
+  const int h = a.by_g.div(hq);
   float q[E], o[E];
   const T* qp = static_cast<const T*>(a.q) + row * a.q_stride + (size_t)hq * D + lane * E;
 #pragma unroll

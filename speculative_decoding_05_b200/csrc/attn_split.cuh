@@ -217,7 +217,7 @@ __global__ void __launch_bounds__(kSplitThreads, 2)
         const int r = i / kChunks, c = i % kChunks;
         uint4 v = make_uint4(0, 0, 0, 0);
         if (r < it.n_rows) {
-          const int rr = it.qt * kRows + r, tok = rr / a.G;
+          const int rr = it.qt * kRows + r, tok = a.by_g.div(rr);
           v = *reinterpret_cast<const uint4*>(static_cast<const T*>(a.q) +
                                               (it.row0 + tok) * a.q_stride +
                                               (it.h * a.G + rr - tok * a.G) * D + 8 * c);
@@ -250,9 +250,9 @@ __global__ void __launch_bounds__(kSplitThreads, 2)
       for (int m = 0; m < MT; ++m)
 #pragma unroll
         for (int x = 0; x < 2; ++x)
-          pos[m][x] = it.past + min((it.qt * kRows + m * 16 + g + 8 * x) / a.G, it.n - 1);
-      const int pos_min = it.past + it.qt * kRows / a.G;
-      const int pos_max = it.past + (it.qt * kRows + it.n_rows - 1) / a.G;
+          pos[m][x] = it.past + min(a.by_g.div(it.qt * kRows + m * 16 + g + 8 * x), it.n - 1);
+      const int pos_min = it.past + a.by_g.div(it.qt * kRows);
+      const int pos_max = it.past + a.by_g.div(it.qt * kRows + it.n_rows - 1);
 
       float o[MT][D / 8][4], mx[MT][2], sum[MT][2];
 #pragma unroll
@@ -525,7 +525,7 @@ __global__ void __launch_bounds__(kSplitThreads, 2)
             const float inv = 1.0f / L;
             v.x *= inv; v.y *= inv; v.z *= inv; v.w *= inv;
             if (!isfinite(v.x) || !isfinite(v.y) || !isfinite(v.z) || !isfinite(v.w)) sm.bad[r] = 1;
-            const int rr = it.qt * kRows + m * 16 + r, tok = rr / a.G;
+            const int rr = it.qt * kRows + m * 16 + r, tok = a.by_g.div(rr);
             T* dst = static_cast<T*>(a.out) +
                      ((it.row0 + tok) * a.Hq + it.h * a.G + rr - tok * a.G) * D + c;
             *reinterpret_cast<uint2*>(dst) =
@@ -541,7 +541,7 @@ __global__ void __launch_bounds__(kSplitThreads, 2)
         if (whole) {
           for (int r = warp; r < 16; r += kSplitWarps) {
             if (!sm.bad[r]) continue;
-            const int rr = it.qt * kRows + m * 16 + r, tok = rr / a.G;
+            const int rr = it.qt * kRows + m * 16 + r, tok = a.by_g.div(rr);
             attend_row<T, TC, D>(a, it.b, it.past + tok, it.h * a.G + rr - tok * a.G,
                                  it.row0 + tok, flags);
           }

@@ -16,10 +16,11 @@
 // one vote a tile finds the rare score that is too far above it (kHot), when
 // the reference is raised and sums and O^T are rescaled.
 //
-// Warps: 8 softmax, 1 producer (TMA), 1 that issues the MMAs, and with an e4m3
-// cache 4 that widen its tiles from the TMA ring into the operand ring.  The
-// operands pass in the order K0 K1 V0 K2 V1 ..: the next tile's scores are
-// formed while this one's weights are.
+// Warps: 8 softmax, one each that loads K (and walks the piece), V and Q, one
+// that issues the MMAs, and with an e4m3 cache 4 that widen its tiles from the
+// TMA ring into the operand ring.  The
+// operands pass in the order K0 K1 K2 V0 K3 V1 ..: scores are formed two tiles
+// ahead, as far as their two buffers reach.
 #pragma once
 
 #include <type_traits>
@@ -31,16 +32,18 @@ namespace dspark {
 
 constexpr int kStepKeys = 128;
 constexpr int kStepSoftmax = 8;                    // warps
-constexpr int kStepProducer = kStepSoftmax;        // warp
-constexpr int kStepMma = kStepSoftmax + 1;         // warp
-constexpr int kStepWiden = kStepSoftmax + 2;       // first of 4 warps, e4m3 only
+constexpr int kStepLoadK = kStepSoftmax;           // warp
+constexpr int kStepLoadV = kStepSoftmax + 1;       // warp
+constexpr int kStepLoadQ = kStepSoftmax + 2;       // warp
+constexpr int kStepMma = kStepSoftmax + 3;         // warp
+constexpr int kStepWiden = kStepSoftmax + 4;       // first of 4 warps, e4m3 only
 constexpr int kStepItems = 4;
 constexpr int kStepScales = 4;
 constexpr int kSmemLimit = 232448;                 // 227 KB a CTA
 
 template <typename TC>
 __host__ __device__ constexpr int step_threads() {
-  return 32 * (kStepSoftmax + 2 + (sizeof(TC) == 1 ? 4 : 0));
+  return 32 * (kStepSoftmax + 4 + (sizeof(TC) == 1 ? 4 : 0));
 }
 
 template <typename TC, int D, int N>
@@ -52,7 +55,10 @@ struct StepCfg {
   static constexpr int kQBytes = N * D * 2;
   static constexpr int kPBytes = kStepKeys * N * 2;
   static constexpr int kSmall = 10240;
-  static constexpr int kLeft = kSmemLimit - 1024 - kSmall - kQBufs * kQBytes - 2 * kPBytes;
+  // 16 KB behind the operands, see StepSmem
+  static constexpr int kPQ = kQBufs * kQBytes + 2 * kPBytes;
+  static constexpr int kBehind = kPQ < 16384 ? 16384 - kPQ : 16;
+  static constexpr int kLeft = kSmemLimit - 1024 - kSmall - kPQ - kBehind;
   static constexpr int kOps = kQ8 ? (kLeft >= 3 * kOpBytes + 3 * kRawBytes ? 3 : 2)
                                   : (kLeft / kOpBytes < 8 ? kLeft / kOpBytes : 8);
   static constexpr int kRawFit = kQ8 ? (kLeft - kOps * kOpBytes) / kRawBytes : 1;
@@ -65,10 +71,11 @@ template <typename TC, int D, int N>
 struct StepSmem {
   using C = StepCfg<TC, D, N>;
   alignas(1024) unsigned char op[C::kOps][C::kOpBytes];
-  // behind the operands: with D = 64 the MMAs of V read 16 KB past a tile (see
-  // the MMA warp), which has to stay inside
+  // with D = 64 the MMAs of V read 16 KB past a tile (see the MMA warp): p, q
+  // and `behind` are as much
   alignas(1024) unsigned char p[2][C::kPBytes];
   alignas(1024) unsigned char q[C::kQBufs][C::kQBytes];
+  unsigned char behind[C::kBehind];
   alignas(1024) unsigned char raw[C::kQ8 ? C::kRaws : 1][C::kQ8 ? C::kRawBytes : 16];
   float scale[C::kQ8 ? kStepScales : 1][2][kStepKeys];
   float m[N], f[N], part[4][N];
@@ -83,26 +90,45 @@ struct StepSmem {
   uint64_t drain;
   Item item[kStepItems];
   Piece piece;
-  long long scan[14];
+  long long scan[16];
   uint32_t tmem;
   unsigned flags;
   int stop;
+  int next_k, next_v;  // operand that the K and the V warp issue next, at least
+  int last_k, last_v, last_tile;
 };
 
-// A step's place in the operand order K0 K1 V0 K2 V1 .. of an item of n tiles.
-__device__ __forceinline__ int op_of_k(int j) { return j == 0 ? 0 : 2 * j - 1; }
-__device__ __forceinline__ int op_of_v(int j, int n) { return j == n - 1 ? 2 * n - 1 : 2 * j + 2; }
+// Place of tile j's K and V in the operand order K0 K1 K2 V0 K3 V1 .. of an item
+// of n tiles, which ends V(n - 2) V(n - 1) (or K0 V0, or K0 K1 V0 V1).
+__device__ __forceinline__ int op_of_k(int j) { return j < 2 ? j : 2 * j - 2; }
+__device__ __forceinline__ int op_of_v(int j, int n) {
+  return j + min(j + 3, n);
+}
+// Whether operand s is a K.
+__device__ __forceinline__ bool op_is_k(int s, int n) {
+  return s < 2 ? s < n : !(s & 1) && s / 2 + 1 < n;
+}
+
+// Bounded wait until another warp has issued every operand up to `op`.
+__device__ __forceinline__ bool next_past(const volatile int* next, int op) {
+  if (*next > op) return true;
+  const uint64_t t0 = global_timer_ns();
+  for (uint32_t i = 1;; ++i) {
+    if (*next > op) return true;
+    if ((i & 255u) == 0 && wait_expired(t0, i)) return false;
+  }
+}
 
 template <typename T, typename TC, int D, int N>
 __global__ void __launch_bounds__(step_threads<TC>(), 1)
     attn_step_kernel(const AttnArgs a, const AttnParts parts, const __grid_constant__ CUtensorMap mk,
-                     const __grid_constant__ CUtensorMap mv, const int box_rows) {
+                     const __grid_constant__ CUtensorMap mv, const int box_shift) {
   using C = StepCfg<TC, D, N>;
   using S = StepSmem<TC, D, N>;
   using TP = typename std::conditional<C::kQ8, __nv_bfloat16, T>::type;  // P and V
   constexpr bool kQ8 = C::kQ8;
   constexpr int kThreads = step_threads<TC>();
-  constexpr int kTmemCols = 4 * N;  // S^T twice, O^T, rounded up to a power of two
+  constexpr int kTmemCols = 4 * N;  // S^T twice, O^T, rounded up to a power of two >= 32
   // A score so far above the reference raises it: 2^64 leaves fp32 sums and
   // bf16 weights far from their ends, 2^14 fp16 ones.
   constexpr float kHot = std::is_same<TP, __half>::value ? 14.0f : 64.0f;
@@ -134,10 +160,12 @@ __global__ void __launch_bounds__(step_threads<TC>(), 1)
     }
     for (int i = 0; i < kStepItems; ++i) {
       mbar_init(&sm.item_full[i], 1);
-      mbar_init(&sm.item_empty[i], kQ8 ? 3 : 2);
+      mbar_init(&sm.item_empty[i], kQ8 ? 5 : 4);
     }
     mbar_init(&sm.drain, 1);
     sm.flags = 0;
+    sm.last_k = sm.last_v = sm.last_tile = -1;
+    sm.next_k = sm.next_v = 0;
     fence_barrier_init();
   }
   if (warp == kStepMma) tmem_alloc(&sm.tmem, kTmemCols);
@@ -148,132 +176,166 @@ __global__ void __launch_bounds__(step_threads<TC>(), 1)
   tc_fence_after();
   const uint32_t tmem = sm.tmem;
 
-  if (warp == kStepProducer) {
-    // ---- producer: item descriptors, Q rows, K and V tiles ----
+  if (warp == kStepLoadK || warp == kStepLoadV) {
+    // ---- loads: items and K tiles (and scales); V tiles ----
     uint64_t* full = kQ8 ? sm.raw_full : sm.op_full;
     uint64_t* empty = kQ8 ? sm.raw_empty : sm.op_empty;
+    const int shift = a.rows.page_shift, in_page = (1 << shift) - 1;
+    const int box_rows = 1 << box_shift;
+    const bool is_k = warp == kStepLoadK;
+    volatile int* my_next = is_k ? &sm.next_k : &sm.next_v;
+    const volatile int* other_next = is_k ? &sm.next_v : &sm.next_k;
     Walk walk;
-    walk.start(a, tiles, sm.piece);
+    if (is_k) walk.start(a, tiles, sm.piece);
     PartRecord rec = {};
     rec.b = -1;
-    int fill = 0, n_item = 0, n_tile = 0;
+    int op0 = 0, tile0 = 0;
     bool alive = true;
-    while (alive) {
-      const Item it = walk.next(a, tiles);
+    for (int n_item = 0; alive; ++n_item) {
       const int slot = n_item % kStepItems;
-      if (n_item >= kStepItems)
-        alive = mbar_wait(&sm.item_empty[slot], (uint32_t)(n_item / kStepItems - 1) & 1u);
-      if (!alive) break;
-      if (lane == 0) {
-        sm.item[slot] = it;
-        mbar_arrive(&sm.item_full[slot]);  // release: the descriptor is visible to the waiters
-      }
-      __syncwarp();
-      if (it.part < 0) break;
-      if (it.part == 1) rec.head = it.part_ends ? 1 : 2;
-      if (it.part == 2) {
-        rec.row0 = it.row0;
-        rec.b = it.b; rec.h = it.h; rec.qt = it.qt;
-        rec.n = it.n; rec.past = it.past; rec.n_rows = it.n_rows;
-      }
-      // page of this lane's box: of the tiles j (its V is next), j + 1, j + 2
-      const int shift = a.rows.page_shift, last_key = it.past + it.n;
-      const int n = it.t1 - it.t0;
-      auto page_of = [&](int j) {
-        const int k = (it.t0 + j) * kStepKeys + lane * box_rows;
-        return j < n && lane * box_rows < kStepKeys && k < last_key
-                   ? __ldg(a.rows.page_table + (size_t)it.b * a.rows.max_pages + (k >> shift))
-                   : 0;
-      };
-      int page0 = page_of(0), page1 = page_of(1), page2 = page_of(2);
-
-      // Q rows, K-major, 128-byte swizzle; rows behind the last are zero
-      const int qb = n_item % C::kQBufs;
-      if (n_item >= C::kQBufs)
-        alive = mbar_wait(&sm.q_empty[qb], (uint32_t)(n_item / C::kQBufs - 1) & 1u);
-      if (!alive) break;
-      {
-        constexpr int kChunks = D / 8, kBatch = 8;
-        for (int i0 = lane; i0 < N * kChunks; i0 += 32 * kBatch) {
-          uint4 v[kBatch];
-#pragma unroll
-          for (int x = 0; x < kBatch; ++x) {
-            const int i = i0 + 32 * x, r = i / kChunks, c = i % kChunks;
-            v[x] = make_uint4(0, 0, 0, 0);
-            if (r < it.n_rows) {
-              const int rr = it.qt * N + r, tok = rr / a.G;
-              v[x] = *reinterpret_cast<const uint4*>(static_cast<const T*>(a.q) +
-                                                     (it.row0 + tok) * a.q_stride +
-                                                     (it.h * a.G + rr - tok * a.G) * D + 8 * c);
-            }
-          }
-#pragma unroll
-          for (int x = 0; x < kBatch; ++x) {
-            const int i = i0 + 32 * x, r = i / kChunks, c = i % kChunks;
-            if (r < N)
-              *reinterpret_cast<uint4*>(sm.q[qb] + sw128_offset(r, 8 * c, N)) = v[x];
-          }
-        }
-        fence_proxy_async_smem();
-        mbar_arrive(&sm.q_full[qb]);
-      }
-      ++n_item;
-
-      for (int s = 0; s < 2 * n; ++s, ++fill) {
-        const bool is_k = s == 0 || ((s & 1) && s != 2 * n - 1);
-        const int j = is_k ? (s + 1) / 2 : s == 2 * n - 1 ? n - 1 : s / 2 - 1;
-        const int t = it.t0 + j;
-        int pid = is_k && j > 0 ? page1 : page0;
-        const int stage = fill % C::kRing;
-        if (fill >= C::kRing)
-          alive = mbar_wait(&empty[stage], (uint32_t)(fill / C::kRing - 1) & 1u);
-        if (alive && kQ8 && is_k && n_tile + j >= kStepScales)
-          alive = mbar_wait(&sm.scale_empty[(n_tile + j) % kStepScales],
-                            (uint32_t)((n_tile + j) / kStepScales - 1) & 1u);
-        if (!alive) break;
-        const int here = min(kStepKeys, last_key - t * kStepKeys);
-        const int boxes = (here + box_rows - 1) / box_rows;
-        const int sc = (n_tile + j) % kStepScales;
+      Item it;
+      if (is_k) {
+        it = walk.next(a, tiles);
+        if (n_item >= kStepItems)
+          alive = mbar_wait(&sm.item_empty[slot], (uint32_t)(n_item / kStepItems - 1) & 1u);
+        if (!__all_sync(0xffffffffu, alive)) break;
         if (lane == 0) {
-          mbar_arrive_expect_tx(&full[stage], boxes * box_rows * D * (int)sizeof(TC));
-          if (kQ8 && is_k) mbar_arrive_expect_tx(&sm.scale_full[sc], 2 * boxes * box_rows * 4);
+          sm.item[slot] = it;
+          mbar_arrive(&sm.item_full[slot]);  // release: the descriptor is visible to the waiters
         }
         __syncwarp();
-        if (lane < boxes) {
-          if (pid < 0 || pid >= a.rows.n_pages) {
-            flags |= DSPARK_FLAG_BAD_PAGE;
-            pid = 0;
-          }
-          const int y = ((pid * a.Hkv + it.h) << shift) +
-                        ((t * kStepKeys + lane * box_rows) & ((1 << shift) - 1));
+        if (it.part == 1) rec.head = it.part_ends ? 1 : 2;
+        if (it.part == 2) {
+          rec.row0 = it.row0;
+          rec.b = it.b; rec.h = it.h; rec.qt = it.qt;
+          rec.n = it.n; rec.past = it.past; rec.n_rows = it.n_rows;
+        }
+      } else {
+        alive = mbar_wait(&sm.item_full[slot], (uint32_t)(n_item / kStepItems) & 1u);
+        if (!__all_sync(0xffffffffu, alive)) break;
+        it = sm.item[slot];
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sm.item_empty[slot]);
+      }
+      if (it.part < 0) break;
+      const int last_key = it.past + it.n;
+      const int n = it.t1 - it.t0;
+      // page of this lane's box in tile j, read two tiles ahead
+      const int* table = a.rows.page_table + (size_t)it.b * a.rows.max_pages;
+      auto page_of = [&](int j) {
+        const int k = (it.t0 + j) * kStepKeys + (lane << box_shift);
+        return j < n && (lane << box_shift) < kStepKeys && k < last_key ? __ldg(table + (k >> shift))
+                                                                        : 0;
+      };
+      int page0 = page_of(0), page1 = page_of(1);
+
+#pragma unroll 1
+      for (int j = 0; j < n; ++j) {
+        const int k0 = (it.t0 + j) * kStepKeys;
+        const int boxes = min((last_key - k0 + box_rows - 1) >> box_shift, kStepKeys >> box_shift);
+        int pid = page0;
+        if (lane < boxes && (unsigned)pid >= (unsigned)a.rows.n_pages) {
+          flags |= DSPARK_FLAG_BAD_PAGE;
+          pid = 0;
+        }
+        const int y_mine = ((pid * a.Hkv + it.h) << shift) + ((k0 + (lane << box_shift)) & in_page);
+        page0 = page1;
+        page1 = page_of(j + 2);
+        int y[kStepKeys / 16];
+#pragma unroll
+        for (int i = 0; i < kStepKeys / 16; ++i) y[i] = __shfl_sync(0xffffffffu, y_mine, i);
+        const int op = op0 + (is_k ? op_of_k(j) : op_of_v(j, n));
+        const int stage = op % C::kRing;
+        // The wait for the stage's release tells phases apart by parity only.
+        // Its last use may be the other warp's: once that is filled the use
+        // before it has been released, and the parity can mean one phase.
+        if (lane == 0) *my_next = op;
+        if (op >= C::kRing) {
+          if (!next_past(other_next, op - C::kRing)) alive = false;
+          if (alive) alive = mbar_wait(&empty[stage], (uint32_t)(op / C::kRing - 1) & 1u);
+        }
+        const int sc = (tile0 + j) % kStepScales;
+        if (alive && kQ8 && is_k && tile0 + j >= kStepScales)
+          alive = mbar_wait(&sm.scale_empty[sc], (uint32_t)((tile0 + j) / kStepScales - 1) & 1u);
+        if (!__all_sync(0xffffffffu, alive)) {
+          alive = false;
+          break;
+        }
+        if (elect_one()) {
+          mbar_arrive_expect_tx(&full[stage], (boxes << box_shift) * D * (int)sizeof(TC));
+          if (kQ8 && is_k) mbar_arrive_expect_tx(&sm.scale_full[sc], (boxes << box_shift) * 8);
           unsigned char* dst = kQ8 ? sm.raw[stage] : sm.op[stage];
+          const CUtensorMap* map = is_k ? &mk : &mv;
           constexpr int kWidth = kQ8 && D == 64 ? 64 : 128;
           constexpr int kHalves = kQ8 ? 1 : D / 64;
 #pragma unroll
-          for (int hf = 0; hf < kHalves; ++hf)
-            tma_load_2d(dst + hf * kStepKeys * 128 + lane * box_rows * kWidth, is_k ? &mk : &mv,
-                        &full[stage], hf * 64, y);
-          if (kQ8 && is_k) {
-            const uint64_t pol = policy_evict_first();
-            bulk_load(&sm.scale[sc][0][lane * box_rows], a.k_scale + y, box_rows * 4,
-                      &sm.scale_full[sc], pol);
-            bulk_load(&sm.scale[sc][1][lane * box_rows], a.v_scale + y, box_rows * 4,
-                      &sm.scale_full[sc], pol);
+          for (int i = 0; i < kStepKeys / 16; ++i) {
+            if (i < boxes) {
+#pragma unroll
+              for (int hf = 0; hf < kHalves; ++hf)
+                tma_load_2d(dst + hf * kStepKeys * 128 + (i << box_shift) * kWidth, map,
+                            &full[stage], hf * 64, y[i]);
+              if (kQ8 && is_k) {
+                const uint64_t pol = policy_evict_first();
+                bulk_load(&sm.scale[sc][0][i << box_shift], a.k_scale + y[i], box_rows * 4,
+                          &sm.scale_full[sc], pol);
+                bulk_load(&sm.scale[sc][1][i << box_shift], a.v_scale + y[i], box_rows * 4,
+                          &sm.scale_full[sc], pol);
+              }
+            }
           }
         }
         __syncwarp();
-        if (!is_k) {
-          page0 = page1;
-          page1 = page2;
-          page2 = page_of(j + 3);
-        }
+        if (is_k) sm.last_k = op;  // for the drain: the operands loaded last
+        else sm.last_v = op;
+        if (is_k) sm.last_tile = tile0 + j;
       }
-      n_tile += n;
+      op0 += 2 * n;
+      tile0 += n;
+      if (lane == 0) *my_next = op0;  // or a later one: the next item says
     }
     if (!alive) flags |= DSPARK_FLAG_TIMEOUT;
-    drain_ring_loads(full, C::kRing, fill);
-    if (kQ8) drain_ring_loads(sm.scale_full, kStepScales, n_tile);
-    if (lane == 0) parts.rec[blockIdx.x] = rec;
+    if (lane == 0 && is_k) parts.rec[blockIdx.x] = rec;
+
+  } else if (warp == kStepLoadQ) {
+    // ---- loads: Q rows, K-major, 128-byte swizzle; rows behind the last are zero ----
+    bool alive = true;
+    for (int n_item = 0;; ++n_item) {
+      const int slot = n_item % kStepItems, qb = n_item % C::kQBufs;
+      alive = mbar_wait(&sm.item_full[slot], (uint32_t)(n_item / kStepItems) & 1u);
+      if (!__all_sync(0xffffffffu, alive)) break;
+      const Item it = sm.item[slot];
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sm.item_empty[slot]);
+      if (it.part < 0) break;
+      if (n_item >= C::kQBufs)
+        alive = mbar_wait(&sm.q_empty[qb], (uint32_t)(n_item / C::kQBufs - 1) & 1u);
+      if (!__all_sync(0xffffffffu, alive)) break;
+      constexpr int kChunks = D / 8, kBatch = 8;
+#pragma unroll 1
+      for (int i0 = lane; i0 < N * kChunks; i0 += 32 * kBatch) {
+        uint4 v[kBatch];
+#pragma unroll
+        for (int x = 0; x < kBatch; ++x) {
+          const int i = i0 + 32 * x, r = i / kChunks, c = i % kChunks;
+          v[x] = make_uint4(0, 0, 0, 0);
+          if (r < it.n_rows) {
+            const int rr = it.qt * N + r, tok = a.by_g.div(rr);
+            v[x] = *reinterpret_cast<const uint4*>(static_cast<const T*>(a.q) +
+                                                   (it.row0 + tok) * a.q_stride +
+                                                   (it.h * a.G + rr - tok * a.G) * D + 8 * c);
+          }
+        }
+#pragma unroll
+        for (int x = 0; x < kBatch; ++x) {
+          const int i = i0 + 32 * x, r = i / kChunks, c = i % kChunks;
+          if (r < N) *reinterpret_cast<uint4*>(sm.q[qb] + sw128_offset(r, 8 * c, N)) = v[x];
+        }
+      }
+      fence_proxy_async_smem();
+      mbar_arrive(&sm.q_full[qb]);
+    }
+    if (!alive) flags |= DSPARK_FLAG_TIMEOUT;
 
   } else if (warp == kStepMma) {
     // ---- MMA issue ----
@@ -283,62 +345,67 @@ __global__ void __launch_bounds__(step_threads<TC>(), 1)
     int op0 = 0, tile0 = 0;
     for (int n_item = 0;; ++n_item) {
       const int slot = n_item % kStepItems;
-      alive = alive && mbar_wait(&sm.item_full[slot], (uint32_t)(n_item / kStepItems) & 1u);
+      if (alive) alive = mbar_wait(&sm.item_full[slot], (uint32_t)(n_item / kStepItems) & 1u);
+      alive = __all_sync(0xffffffffu, alive);
       if (!alive) break;
       const int part = sm.item[slot].part, n = sm.item[slot].t1 - sm.item[slot].t0;
       __syncwarp();
       if (lane == 0) mbar_arrive(&sm.item_empty[slot]);
       if (part < 0) break;
-      if (lane == 0) {
-        const int qb = n_item % C::kQBufs;
-        auto wait = [&](uint64_t* bar, uint32_t parity) {
-          if (alive) alive = mbar_wait_spin(bar, parity);
-        };
-        auto issue_s = [&](int j) {
-          const int op = op0 + op_of_k(j), os = op % C::kOps, buf = (tile0 + j) & 1;
-          wait(&sm.op_full[os], (uint32_t)(op / C::kOps) & 1u);
-          if (!alive) return;
-          tc_fence_after();
-          const uint32_t kb = smem_u32(sm.op[os]), qa = smem_u32(sm.q[qb]);
+      const int qb = n_item % C::kQBufs;
+      auto wait = [&](uint64_t* bar, uint32_t parity) {
+        if (alive) alive = mbar_wait_spin(bar, parity);
+        alive = __all_sync(0xffffffffu, alive);
+      };
+      auto issue_s = [&](int j) {
+        const int op = op0 + op_of_k(j), os = op % C::kOps, buf = (tile0 + j) & 1;
+        wait(&sm.op_full[os], (uint32_t)(op / C::kOps) & 1u);
+        tc_fence_after();
+        const uint64_t kd = sdesc_sw128(smem_u32(sm.op[os])), qd = sdesc_sw128(smem_u32(sm.q[qb]));
+        if (alive && elect_one()) {
 #pragma unroll
           for (int k = 0; k < D / 16; ++k)
-            mma_bf16_ss(tmem + buf * N, sdesc_sw128(kb + (k >> 2) * kStepKeys * 128 + (k & 3) * 32),
-                        sdesc_sw128(qa + (k >> 2) * N * 128 + (k & 3) * 32), kIdS, k > 0);
+            mma_bf16_ss(tmem + buf * N, kd + (((k >> 2) * kStepKeys * 128 + (k & 3) * 32) >> 4),
+                        qd + (((k >> 2) * N * 128 + (k & 3) * 32) >> 4), kIdS, k > 0);
           mma_commit(&sm.op_empty[os]);
           mma_commit(&sm.s_full[buf]);
-        };
-        wait(&sm.q_full[qb], (uint32_t)(n_item / C::kQBufs) & 1u);
-        issue_s(0);
-        for (int j = 0; j < n; ++j) {
-          // scores of the next tile: its buffer was read before the weights of
-          // tile j - 1 were announced
-          if (j + 1 < n) issue_s(j + 1);
-          if (j + 1 == n && alive) mma_commit(&sm.q_empty[qb]);
-          const int g = tile0 + j, buf = g & 1;
-          const int op = op0 + op_of_v(j, n), os = op % C::kOps;
-          wait(&sm.op_full[os], (uint32_t)(op / C::kOps) & 1u);
-          wait(&sm.p_full[buf], (uint32_t)(g >> 1) & 1u);
-          if (!alive) break;
-          tc_fence_after();
-          const uint32_t vb = smem_u32(sm.op[os]), pb = smem_u32(sm.p[buf]);
-          // V: 64 elements of D in a row, 8 keys 1024 bytes apart, the other 64
-          // behind all keys.  With D = 64 there are no others: lanes 64-127 of
-          // O^T take what lies there and nobody reads them.
+          if (j == n - 1) mma_commit(&sm.q_empty[qb]);
+        }
+        __syncwarp();
+      };
+      wait(&sm.q_full[qb], (uint32_t)(n_item / C::kQBufs) & 1u);
+      issue_s(0);
+      if (n > 1) issue_s(1);
+      for (int j = 0; j < n; ++j) {
+        const int g = tile0 + j, buf = g & 1;
+        wait(&sm.p_full[buf], (uint32_t)(g >> 1) & 1u);
+        // the scores of tile j were read: their buffer takes those of j + 2
+        if (j + 2 < n) issue_s(j + 2);
+        const int op = op0 + op_of_v(j, n), os = op % C::kOps;
+        wait(&sm.op_full[os], (uint32_t)(op / C::kOps) & 1u);
+        tc_fence_after();
+        // V: 64 elements of D in a row, 8 keys 1024 bytes apart, the other 64
+        // behind all keys.  With D = 64 there are no others: lanes 64-127 of
+        // O^T take what lies there and nobody reads them.
+        constexpr int kW = N < 64 ? N : 64;  // rows of P^T in a row of shared memory
+        const uint64_t vd = sdesc_mn<64>(smem_u32(sm.op[os]), kStepKeys);
+        const uint64_t pd = sdesc_mn<kW>(smem_u32(sm.p[buf]), kStepKeys);
+        if (alive && elect_one()) {
 #pragma unroll
           for (int k = 0; k < kStepKeys / 16; ++k)
-            mma_bf16_ss(tmem + 2 * N, sdesc_mn<64>(vb + k * 2048, kStepKeys),
-                        sdesc_mn<(N < 64 ? N : 64)>(pb + k * 16 * (N < 64 ? N : 64) * 2, kStepKeys),
-                        kIdO, j > 0 || k > 0);
+            mma_bf16_ss(tmem + 2 * N, vd + ((k * 2048) >> 4), pd + ((k * 16 * kW * 2) >> 4), kIdO,
+                        j > 0 || k > 0);
           mma_commit(&sm.op_empty[os]);
           mma_commit(&sm.p_empty[buf]);
         }
+        __syncwarp();
       }
-      alive = __shfl_sync(0xffffffffu, (int)alive, 0) != 0;
       op0 += 2 * n;
       tile0 += n;
     }
     if (!alive) flags |= DSPARK_FLAG_TIMEOUT;
-    if (lane == 0) drain_mma(&sm.drain);
+    // every commit above was the elected lane's: so is the last one
+    if (elect_one()) drain_mma(&sm.drain);
     __syncwarp();
 
   } else if (warp >= kStepWiden) {
@@ -359,7 +426,7 @@ __global__ void __launch_bounds__(step_threads<TC>(), 1)
         if (tid == 0) mbar_arrive(&sm.item_empty[slot]);
         if (part < 0) break;
         for (int s = 0; s < 2 * n && alive; ++s, ++op) {
-          const bool is_k = s == 0 || ((s & 1) && s != 2 * n - 1);
+          const bool is_k = op_is_k(s, n);
           const int rs = op % C::kRaws, os = op % C::kOps;
           alive = mbar_wait(&sm.raw_full[rs], (uint32_t)(op / C::kRaws) & 1u);
           if (alive && op >= C::kOps)
@@ -405,7 +472,7 @@ __global__ void __launch_bounds__(step_threads<TC>(), 1)
       const Item it = sm.item[slot];
       if (threadIdx.x < N) {
         const int n = threadIdx.x;
-        const int rr = it.qt * N + min(n, it.n_rows - 1), tok = rr / a.G;
+        const int rr = it.qt * N + min(n, it.n_rows - 1), tok = a.by_g.div(rr);
         const int p = it.past + tok;
         sm.pos[n] = p;
         sm.low[n] = first_seen(p, a.window);
@@ -416,8 +483,8 @@ __global__ void __launch_bounds__(step_threads<TC>(), 1)
       named_sync(1, 32 * kStepSoftmax);
       if (threadIdx.x == 0) mbar_arrive(&sm.item_empty[slot]);
       const int nt = it.t1 - it.t0;
-      const int pos_min = it.past + it.qt * N / a.G;
-      const int pos_max = it.past + (it.qt * N + it.n_rows - 1) / a.G;
+      const int pos_min = it.past + a.by_g.div(it.qt * N);
+      const int pos_max = it.past + a.by_g.div(it.qt * N + it.n_rows - 1);
       float l[R];
 #pragma unroll
       for (int i = 0; i < R; ++i) l[i] = 0.0f;
@@ -595,12 +662,12 @@ __global__ void __launch_bounds__(step_threads<TC>(), 1)
       named_sync(bar_wg, 128);
       if (key < D) {  // uniform over a warp
 #pragma unroll
-        for (int c = 0; c < R; c += kChunk32) {
+        for (int c = 0; c < R; c += 8) {
           if (n0 + c >= it.n_rows) break;
-          uint32_t o[kChunk32];
-          tmem_ld<kChunk32>(tmem + lane_base + 2 * N + n0 + c, o);
+          uint32_t o[8];
+          tmem_ld<8>(tmem + lane_base + 2 * N + n0 + c, o);
 #pragma unroll
-          for (int i = 0; i < kChunk32; ++i) {
+          for (int i = 0; i < 8; ++i) {
             const int n = n0 + c + i;
             if (n < it.n_rows) {
               if (whole) {
@@ -621,7 +688,7 @@ __global__ void __launch_bounds__(step_threads<TC>(), 1)
       if (whole) {
         for (int n = n0 + quarter; n < n0 + R && n < it.n_rows; n += 4) {
           if (!sm.bad[n]) continue;
-          const int rr = it.qt * N + n, tok = rr / a.G;
+          const int rr = it.qt * N + n, tok = a.by_g.div(rr);
           attend_row<T, TC, D>(a, it.b, it.past + tok, it.h * a.G + rr - tok * a.G, it.row0 + tok,
                                flags);
         }
@@ -632,6 +699,19 @@ __global__ void __launch_bounds__(step_threads<TC>(), 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
+  // after an abort copies may still be in flight: none outlives the CTA
+  if (sm.flags & DSPARK_FLAG_TIMEOUT) {
+    if (threadIdx.x == 0) {
+      uint64_t* full = kQ8 ? sm.raw_full : sm.op_full;
+      const int last = max(sm.last_k, sm.last_v);
+      for (int op = max(last - C::kRing + 1, 0); op <= last; ++op)
+        mbar_wait(&full[op % C::kRing], (uint32_t)(op / C::kRing) & 1u);
+      if (kQ8)
+        for (int t = max(sm.last_tile - kStepScales + 1, 0); t <= sm.last_tile; ++t)
+          mbar_wait(&sm.scale_full[t % kStepScales], (uint32_t)(t / kStepScales) & 1u);
+    }
+    __syncthreads();
+  }
   if (warp == kStepMma) tmem_dealloc(tmem, kTmemCols);
   if (threadIdx.x == 0) store_status(a.status, sm.flags);
 }

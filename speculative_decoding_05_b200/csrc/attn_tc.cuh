@@ -20,18 +20,18 @@ __host__ __device__ constexpr uint32_t idesc_tc(int M, int N, bool a_mn, bool b_
 }
 
 // Shared-memory descriptor of an operand whose M or N dimension is contiguous:
-// rows (of K) of W elements, swizzled over their 2 W bytes (W = 64 or 32), 8
+// rows (of K) of W elements, swizzled over their 2 W bytes (W 64, 32 or 16), 8
 // rows an atom, atoms of further K behind each other; the next W elements of M
 // or N lie `k_rows` rows on.
 template <int W>
 __device__ __forceinline__ uint64_t sdesc_mn(uint32_t addr, int k_rows) {
-  static_assert(W == 64 || W == 32, "row width");
+  static_assert(W == 64 || W == 32 || W == 16, "row width");
   uint64_t d = 0;
   d |= (uint64_t)((addr & 0x3FFFFu) >> 4);
   d |= (uint64_t)((uint32_t)(k_rows * W * 2) >> 4) << 16;  // next W elements
   d |= (uint64_t)((8 * W * 2) >> 4) << 32;                 // next 8 rows
   d |= (uint64_t)1 << 46;
-  d |= (uint64_t)(W == 64 ? 2 : 4) << 61;
+  d |= (uint64_t)(W == 64 ? 2 : W == 32 ? 4 : 6) << 61;
   return d;
 }
 // Byte offset of element (n, k) of such an operand with k_rows rows, n a
@@ -39,33 +39,62 @@ __device__ __forceinline__ uint64_t sdesc_mn(uint32_t addr, int k_rows) {
 template <int W>
 __device__ __forceinline__ uint32_t mn_offset(int n, int k, int k_rows) {
   const int block = n / W, c = (n % W) >> 3;
-  const int sw = W == 64 ? (k & 7) : ((k >> 1) & 3);
+  const int sw = W == 64 ? (k & 7) : W == 32 ? ((k >> 1) & 3) : ((k >> 2) & 1);
   return (uint32_t)(block * k_rows * W * 2 + k * W * 2 + ((c ^ sw) << 4));
+}
+
+// One lane of a converged warp, chosen by the hardware: the compiler knows that
+// a branch on it has a single active thread and issues TMA and MMA instructions
+// in it directly.  Behind `lane == 0` it wraps each of them in a loop over the
+// active lanes, which measured 100 to 150 clocks an instruction.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(r));
+  return r != 0;
 }
 
 template <int C>
 __device__ __forceinline__ void tmem_ld(uint32_t addr, uint32_t (&r)[C]) {
-  static_assert(C == 16 || C == 32, "columns");
+  static_assert(C == 8 || C == 16 || C == 32, "columns");
   if constexpr (C == 32) {
     tmem_ld32_issue(addr, r);
     tmem_ld32_wait(r);
-  } else {
+  } else if constexpr (C == 16) {
     tmem_ld16_issue(addr, r);
     tmem_ld16_wait(r);
+  } else {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];\n\t"
+        "tcgen05.wait::ld.sync.aligned;"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+          "=r"(r[7])
+        : "r"(addr)
+        : "memory");
   }
-}
-__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
-      "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
-      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
-      "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
-      : "memory");
 }
 template <int C>
 __device__ __forceinline__ void tmem_st(uint32_t addr, const uint32_t (&r)[C]) {
-  if constexpr (C == 32) tmem_st32(addr, r);
-  else tmem_st16(addr, r);
+  static_assert(C == 8 || C == 16 || C == 32, "columns");
+  if constexpr (C == 32) {
+    tmem_st32(addr, r);
+  } else if constexpr (C == 16) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+        "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(addr),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+        "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]),
+        "r"(r[15])
+        : "memory");
+  } else {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(addr),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+        : "memory");
+  }
 }
 
 // Whether `p` holds for any of the `count` threads at named barrier `id`.
@@ -88,9 +117,8 @@ __device__ __forceinline__ float warp_max_redux(float v) {
   return r;
 }
 
-// Sums of v[i] over the warp, that of v[i] in lane i (C = 32), or in lanes i
-// and i + 16 (C = 16): at each step a lane keeps half of its values and adds
-// the other lane's.
+// Sums of v[i] over the warp, that of v[i] in the lanes that are i modulo C: at
+// each step a lane keeps half of its values and adds the other lane's.
 template <int C>
 __device__ __forceinline__ float lanes_reduce(float (&v)[C], int lane) {
 #pragma unroll
@@ -103,7 +131,8 @@ __device__ __forceinline__ float lanes_reduce(float (&v)[C], int lane) {
     }
   }
   float s = v[0];
-  if (C == 16) s += __shfl_xor_sync(0xffffffffu, s, 16);
+#pragma unroll
+  for (int w = C; w < 32; w <<= 1) s += __shfl_xor_sync(0xffffffffu, s, w);
   return s;
 }
 

@@ -160,8 +160,6 @@ struct LaunchRead {
 constexpr int kAttnMaxSms = 148;
 int attn_sms() { return kv_sms() < kAttnMaxSms ? kv_sms() : kAttnMaxSms; }
 
-constexpr int kSplitMaxRows = 32;
-
 struct LaunchAttn {
   AttnArgs a;
   long long rows_per_head;  // at most, of one request
@@ -223,14 +221,17 @@ struct LaunchAttn {
     CUtensorMap mk, mv;
     int box;
     if (!maps<T, TC>(&mk, &mv, t.keys, &box)) return DSPARK_ERR_CUDA;
+    int box_shift = 0;
+    while (1 << box_shift < box) ++box_shift;
     const dspark_status st = launched(launch_dependent(attn_step_kernel<T, TC, Dh, N>, dim3(ctas),
                                                        dim3(step_threads<TC>()), smem, s, a, p, mk,
-                                                       mv, box));
+                                                       mv, box_shift));
     return st != DSPARK_OK ? st : join<T, TC, Dh>(t, p, ctas);
   }
 
   template <typename T, typename TC, int Dh>
   dspark_status run() {
+    if (rows_per_head <= 16) return step<T, TC, Dh, 16>();
     if (rows_per_head <= 32) return step<T, TC, Dh, 32>();
     if (rows_per_head <= 64) return step<T, TC, Dh, 64>();
     return step<T, TC, Dh, 128>();
@@ -395,6 +396,7 @@ dspark_status dspark_attn_verify(
   a.status = static_cast<unsigned*>(workspace);
   a.scale2 = sm_scale * kLog2e;
   a.Hq = Hq; a.Hkv = Hkv; a.G = Hq / Hkv;
+  a.by_g = make_divisor(a.G);
   a.window = window;
   if (n_rows * Hq >= (1ll << 31)) return DSPARK_ERR_UNSUPPORTED;
   l.rows_per_head = (max_len < n_rows ? max_len : n_rows) * a.G;

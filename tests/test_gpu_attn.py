@@ -264,3 +264,22 @@ def test_other_stream_and_two_calls_at_once():
         check(p1, o1, r1)
         check(p2, o2, r2)
         check(p2, o3, r2)
+
+
+@pytest.mark.parametrize("cache", [BF, E4])
+@pytest.mark.parametrize("D_", [64, 128])
+@pytest.mark.parametrize("G,n", [(1, 9), (4, 7), (5, 9), (4, 17), (4, 90)])
+def test_many_short_items_back_to_back(cache, D_, G, n):
+    """Items of one to a few key tiles, calls behind each other without a
+    pause: the rings pass from item to item and from call to call."""
+    g = torch.Generator().manual_seed(G + n)
+    B = 250 if n < 90 else 40
+    new = torch.randint(0, n + 1, (B,), generator=g).tolist()
+    new[0] = n
+    past = torch.randint(0, 500, (B,), generator=g).tolist()
+    p = Problem(new, past, 4 * G, 4, D_, BF, cache, 32, seed=23)
+    first = run(p)
+    outs = [attend(p)[0] for _ in range(20)]
+    torch.cuda.synchronize()
+    for o in outs:
+        assert torch.equal(o, first)
