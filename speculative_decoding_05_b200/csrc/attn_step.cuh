@@ -9,18 +9,29 @@
 //   S^T [128 keys, N rows] = K Q^T      both K-major as they lie in memory
 //   O^T [D, N rows]      += V^T P^T     V as it lies (its MN-major form), P^T
 //                                       [128 keys][N rows] written by the threads
+//   L   [., N rows]      += 1 P^T       the weights' sums, alike in every lane
+//                                       (e4m3: summed by the threads)
 // A thread owns one key and N / 2 rows of S^T (two warpgroups share the rows).
-// The softmax reference of a row then lives across threads, so it is not the
-// running maximum but any earlier maximum (of the item's first tile, as a
-// rule): weights may exceed 1, which costs no precision in floating point, and
-// one vote a tile finds the rare score that is too far above it (kHot), when
-// the reference is raised and sums and O^T are rescaled.
+// A row's softmax then lies across threads, so its reference is not the running
+// maximum: weights are 2^(s - m) with m = 0 to begin with, which costs no
+// precision in floating point while scores stay within 2^+-kHot, and one vote a
+// tile finds the rare tile with a score outside, where m moves to the maximum
+// and O^T and L are rescaled.  (fp16 weights have a short range: there m starts
+// at the maximum of the first tile.)
+//
+// e4m3 cache: S^T takes K's codes as they lie, by the 8-bit MMA, and Q as a sum
+// of two e4m3 parts (three for fp16): Q's row, scaled by a power of two to a
+// maximum in [128, 256), is rounded to e4m3 (4 significant bits), the rest
+// rounded again (4 more).  bf16 has 8 and fp16 11 bits, so the sum is exact for
+// elements down to 2^-9 (2^-6) of the row's maximum; below that it is off by at
+// most 2^-17 of the maximum, less than what bf16 itself (2^-8 of the element)
+// rounds off a row of such a spread.  K's scale is applied to the scores.  P is
+// bf16 with V's scale on it, so V's codes are widened, by 4 warps.
 //
 // Warps: 8 softmax, one each that loads K (and walks the piece), V and Q, one
-// that issues the MMAs, and with an e4m3 cache 4 that widen its tiles from the
-// TMA ring into the operand ring.  The
-// operands pass in the order K0 K1 K2 V0 K3 V1 ..: scores are formed two tiles
-// ahead, as far as their two buffers reach.
+// that issues the MMAs, 4 that widen V (e4m3).  The operands pass in the order
+// K0 K1 K2 V0 K3 V1 ..: scores are formed two tiles ahead, as far as their two
+// buffers reach.
 #pragma once
 
 #include <type_traits>
@@ -46,47 +57,61 @@ __host__ __device__ constexpr int step_threads() {
   return 32 * (kStepSoftmax + 4 + (sizeof(TC) == 1 ? 4 : 0));
 }
 
-template <typename TC, int D, int N>
+// Shared memory.  A 16-bit cache has one ring of operand tiles for K and V.  An
+// e4m3 cache has a ring of K tiles, one of V tiles as they come, and one of
+// widened V tiles.
+template <typename T, typename TC, int D, int N>
 struct StepCfg {
   static constexpr bool kQ8 = sizeof(TC) == 1;
-  static constexpr int kOpBytes = kStepKeys * D * 2;
-  static constexpr int kRawBytes = kQ8 ? kStepKeys * D : 0;
+  static constexpr int kQParts = !kQ8 ? 1 : std::is_same<T, __half>::value ? 3 : 2;
+  static constexpr int kTile = kStepKeys * D * 2;            // an operand tile of 16 bits
+  static constexpr int kTileIn = kStepKeys * D * (int)sizeof(TC);  // a tile as TMA brings it
   static constexpr int kQBufs = N <= 64 ? 2 : 1;
-  static constexpr int kQBytes = N * D * 2;
+  static constexpr int kQBytes = N * D * (kQ8 ? kQParts : 2);
   static constexpr int kPBytes = kStepKeys * N * 2;
+  // the MMA of L (16 bits) takes its ones from TMEM while that has room for them
+  static constexpr bool kOnesInTmem = !kQ8 && N <= 64;
+  static constexpr int kOnes = kQ8 || kOnesInTmem ? 0 : kStepKeys * 128;
+  // S^T twice, O^T, L, ones; without the last two: 3 N, to a power of two
+  static constexpr int kTmemCols = kQ8 ? (N <= 64 ? 4 * N : 512) : N <= 16 ? 128 : N <= 32 ? 256 : 512;
   static constexpr int kSmall = 10240;
-  // 16 KB behind the operands, see StepSmem
-  static constexpr int kPQ = kQBufs * kQBytes + 2 * kPBytes;
+  // 16 KB behind the 16-bit tiles, see StepSmem
+  static constexpr int kPQ = kQBufs * kQBytes + 2 * kPBytes + kOnes;
   static constexpr int kBehind = kPQ < 16384 ? 16384 - kPQ : 16;
   static constexpr int kLeft = kSmemLimit - 1024 - kSmall - kPQ - kBehind;
-  static constexpr int kOps = kQ8 ? (kLeft >= 3 * kOpBytes + 3 * kRawBytes ? 3 : 2)
-                                  : (kLeft / kOpBytes < 8 ? kLeft / kOpBytes : 8);
-  static constexpr int kRawFit = kQ8 ? (kLeft - kOps * kOpBytes) / kRawBytes : 1;
-  static constexpr int kRaws = kRawFit < 8 ? kRawFit : 8;
-  static constexpr int kRing = kQ8 ? kRaws : kOps;  // the ring that TMA fills
-  static_assert(kOps >= 2 && kRaws >= 1, "shared memory");
+  static constexpr int kOps = kQ8 ? 2 : kLeft / kTile < 8 ? kLeft / kTile : 8;
+  static constexpr int kInFit = kQ8 ? (kLeft - kOps * kTile) / kTileIn : 0;
+  static constexpr int kIn = kInFit < 16 ? kInFit : 16;
+  static constexpr int kRingK = kQ8 ? (kIn + 1) / 2 : kOps;
+  static constexpr int kRingV = kQ8 ? kIn / 2 : kOps;
+  static_assert(kOps >= 2 && kRingV >= 1, "shared memory");
 };
 
-template <typename TC, int D, int N>
+template <typename T, typename TC, int D, int N>
 struct StepSmem {
-  using C = StepCfg<TC, D, N>;
-  alignas(1024) unsigned char op[C::kOps][C::kOpBytes];
-  // with D = 64 the MMAs of V read 16 KB past a tile (see the MMA warp): p, q
-  // and `behind` are as much
+  using C = StepCfg<T, TC, D, N>;
+  alignas(1024) unsigned char op[C::kOps][C::kTile];
+  // with D = 64 the MMAs of V read 16 KB past a tile (see the MMA warp): p, q,
+  // ones and `behind` are as much
   alignas(1024) unsigned char p[2][C::kPBytes];
   alignas(1024) unsigned char q[C::kQBufs][C::kQBytes];
+  alignas(1024) unsigned char ones[C::kOnes ? C::kOnes : 16];
   unsigned char behind[C::kBehind];
-  alignas(1024) unsigned char raw[C::kQ8 ? C::kRaws : 1][C::kQ8 ? C::kRawBytes : 16];
+  alignas(1024) unsigned char in_k[C::kQ8 ? C::kRingK : 1][C::kQ8 ? C::kTileIn : 16];
+  alignas(1024) unsigned char in_v[C::kQ8 ? C::kRingV : 1][C::kQ8 ? C::kTileIn : 16];
   float scale[C::kQ8 ? kStepScales : 1][2][kStepKeys];
+  float qs[C::kQBufs][N];           // e4m3: power of two that was taken off a row of Q
   float m[N], f[N], part[4][N];
   int pos[N], low[N], bad[N];
   long long out[N];
+  uint64_t k_full[C::kRingK], k_empty[C::kRingK];  // 16 bits: of the common ring
+  uint64_t v_full[C::kRingV], v_empty[C::kRingV];  // e4m3 only, as the next
   uint64_t op_full[C::kOps], op_empty[C::kOps];
-  uint64_t raw_full[C::kRaws], raw_empty[C::kRaws];
   uint64_t scale_full[kStepScales], scale_empty[kStepScales];
   uint64_t q_full[2], q_empty[2];
   uint64_t s_full[2], p_full[2], p_empty[2];
   uint64_t item_full[kStepItems], item_empty[kStepItems];
+  uint64_t v_clean[kStepItems];     // 16 bits: an item's last V tile is cleared behind its end
   uint64_t drain;
   Item item[kStepItems];
   Piece piece;
@@ -94,19 +119,18 @@ struct StepSmem {
   uint32_t tmem;
   unsigned flags;
   int stop;
-  int next_k, next_v;  // operand that the K and the V warp issue next, at least
-  int last_k, last_v, last_tile;
+  int next_k, next_v;               // operand that the K and the V warp issue next, at least
+  int last_k, last_v, last_tile;    // issued last
 };
 
 // Place of tile j's K and V in the operand order K0 K1 K2 V0 K3 V1 .. of an item
 // of n tiles, which ends V(n - 2) V(n - 1) (or K0 V0, or K0 K1 V0 V1).
 __device__ __forceinline__ int op_of_k(int j) { return j < 2 ? j : 2 * j - 2; }
-__device__ __forceinline__ int op_of_v(int j, int n) {
-  return j + min(j + 3, n);
-}
-// Whether operand s is a K.
-__device__ __forceinline__ bool op_is_k(int s, int n) {
-  return s < 2 ? s < n : !(s & 1) && s / 2 + 1 < n;
+__device__ __forceinline__ int op_of_v(int j, int n) { return j + min(j + 3, n); }
+
+// Whether the last tile of an item's part has places behind the sequence.
+__device__ __forceinline__ bool has_tail(const Item& it) {
+  return it.t1 * kStepKeys > it.past + it.n;
 }
 
 // Bounded wait until another warp has issued every operand up to `op`.
@@ -123,29 +147,35 @@ template <typename T, typename TC, int D, int N>
 __global__ void __launch_bounds__(step_threads<TC>(), 1)
     attn_step_kernel(const AttnArgs a, const AttnParts parts, const __grid_constant__ CUtensorMap mk,
                      const __grid_constant__ CUtensorMap mv, const int box_shift) {
-  using C = StepCfg<TC, D, N>;
-  using S = StepSmem<TC, D, N>;
+  using C = StepCfg<T, TC, D, N>;
+  using S = StepSmem<T, TC, D, N>;
   using TP = typename std::conditional<C::kQ8, __nv_bfloat16, T>::type;  // P and V
   constexpr bool kQ8 = C::kQ8;
   constexpr int kThreads = step_threads<TC>();
-  constexpr int kTmemCols = 4 * N;  // S^T twice, O^T, rounded up to a power of two >= 32
-  // A score so far above the reference raises it: 2^64 leaves fp32 sums and
-  // bf16 weights far from their ends, 2^14 fp16 ones.
-  constexpr float kHot = std::is_same<TP, __half>::value ? 14.0f : 64.0f;
+  constexpr int kColO = 2 * N, kColL = 3 * N, kColOnes = 4 * N;  // TMEM: S^T twice, O^T, L, ones
+  constexpr bool kHalfP = std::is_same<TP, __half>::value;
+  // Scores this far over the reference move it: 2^64 leaves fp32 sums and bf16
+  // weights far from their ends, 2^14 fp16 ones.  At the first keys of a row a
+  // score as far below it does so too (fp16: always).
+  constexpr float kHot = kHalfP ? 14.0f : 64.0f;
   extern __shared__ unsigned char smem_raw[];
   S& sm = *reinterpret_cast<S*>(smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u));
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const AttnTiles tiles = {N, kStepKeys};
+  constexpr AttnTiles tiles = {N, kStepKeys};
   unsigned flags = 0;
 
   if (threadIdx.x == 0) {
-    for (int i = 0; i < C::kOps; ++i) {
-      mbar_init(&sm.op_full[i], kQ8 ? 4 : 1);
-      mbar_init(&sm.op_empty[i], 1);
+    for (int i = 0; i < C::kRingK; ++i) {
+      mbar_init(&sm.k_full[i], 1);
+      mbar_init(&sm.k_empty[i], 1);
     }
-    for (int i = 0; i < C::kRaws; ++i) {
-      mbar_init(&sm.raw_full[i], 1);
-      mbar_init(&sm.raw_empty[i], 4);
+    for (int i = 0; i < C::kRingV; ++i) {
+      mbar_init(&sm.v_full[i], 1);
+      mbar_init(&sm.v_empty[i], 4);
+    }
+    for (int i = 0; i < C::kOps; ++i) {
+      mbar_init(&sm.op_full[i], 4);
+      mbar_init(&sm.op_empty[i], 1);
     }
     for (int i = 0; i < kStepScales; ++i) {
       mbar_init(&sm.scale_full[i], 1);
@@ -153,13 +183,14 @@ __global__ void __launch_bounds__(step_threads<TC>(), 1)
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&sm.q_full[i], 32);
-      mbar_init(&sm.q_empty[i], 1);
+      mbar_init(&sm.q_empty[i], kQ8 ? 1 + kStepSoftmax : 1);
       mbar_init(&sm.s_full[i], 1);
       mbar_init(&sm.p_full[i], 32 * kStepSoftmax);
       mbar_init(&sm.p_empty[i], 1);
     }
     for (int i = 0; i < kStepItems; ++i) {
       mbar_init(&sm.item_full[i], 1);
+      mbar_init(&sm.v_clean[i], 32);
       mbar_init(&sm.item_empty[i], kQ8 ? 5 : 4);
     }
     mbar_init(&sm.drain, 1);
@@ -168,21 +199,37 @@ __global__ void __launch_bounds__(step_threads<TC>(), 1)
     sm.next_k = sm.next_v = 0;
     fence_barrier_init();
   }
-  if (warp == kStepMma) tmem_alloc(&sm.tmem, kTmemCols);
+  if (warp == kStepMma) tmem_alloc(&sm.tmem, C::kTmemCols);
+  constexpr uint32_t kOne2 = kHalfP ? 0x3c003c00u : 0x3f803f80u;
+  if constexpr (C::kOnes > 0) {
+    for (int i = threadIdx.x; i < C::kOnes / 16; i += kThreads)
+      reinterpret_cast<uint4*>(sm.ones)[i] = make_uint4(kOne2, kOne2, kOne2, kOne2);
+    fence_proxy_async_smem();
+  }
   grid_dep_launch();
   grid_dep_wait();
   tc_fence_before();
   find_piece<kThreads>(a, tiles, sm.scan, &sm.piece, flags);  // syncs the block
   tc_fence_after();
   const uint32_t tmem = sm.tmem;
+  if constexpr (C::kOnesInTmem) {
+    if (warp < 4) {
+      uint32_t o[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) o[i] = kOne2;
+      tmem_st<8>(tmem + ((uint32_t)(warp * 32) << 16) + kColOnes, o);
+      tmem_st_wait();
+      tc_fence_before();  // the MMAs that read them come behind p_full
+    }
+  }
 
   if (warp == kStepLoadK || warp == kStepLoadV) {
     // ---- loads: items and K tiles (and scales); V tiles ----
-    uint64_t* full = kQ8 ? sm.raw_full : sm.op_full;
-    uint64_t* empty = kQ8 ? sm.raw_empty : sm.op_empty;
     const int shift = a.rows.page_shift, in_page = (1 << shift) - 1;
     const int box_rows = 1 << box_shift;
     const bool is_k = warp == kStepLoadK;
+    uint64_t* full = kQ8 && !is_k ? sm.v_full : sm.k_full;
+    uint64_t* empty = kQ8 && !is_k ? sm.v_empty : sm.k_empty;
     volatile int* my_next = is_k ? &sm.next_k : &sm.next_v;
     const volatile int* other_next = is_k ? &sm.next_v : &sm.next_k;
     Walk walk;
@@ -198,7 +245,10 @@ __global__ void __launch_bounds__(step_threads<TC>(), 1)
         it = walk.next(a, tiles);
         if (n_item >= kStepItems)
           alive = mbar_wait(&sm.item_empty[slot], (uint32_t)(n_item / kStepItems - 1) & 1u);
-        if (!__all_sync(0xffffffffu, alive)) break;
+        if (!__all_sync(0xffffffffu, alive)) {
+          alive = false;
+          break;
+        }
         if (lane == 0) {
           sm.item[slot] = it;
           mbar_arrive(&sm.item_full[slot]);  // release: the descriptor is visible to the waiters
@@ -212,7 +262,10 @@ __global__ void __launch_bounds__(step_threads<TC>(), 1)
         }
       } else {
         alive = mbar_wait(&sm.item_full[slot], (uint32_t)(n_item / kStepItems) & 1u);
-        if (!__all_sync(0xffffffffu, alive)) break;
+        if (!__all_sync(0xffffffffu, alive)) {
+          alive = false;
+          break;
+        }
         it = sm.item[slot];
         __syncwarp();
         if (lane == 0) mbar_arrive(&sm.item_empty[slot]);
@@ -244,15 +297,18 @@ __global__ void __launch_bounds__(step_threads<TC>(), 1)
         int y[kStepKeys / 16];
 #pragma unroll
         for (int i = 0; i < kStepKeys / 16; ++i) y[i] = __shfl_sync(0xffffffffu, y_mine, i);
-        const int op = op0 + (is_k ? op_of_k(j) : op_of_v(j, n));
-        const int stage = op % C::kRing;
-        // The wait for the stage's release tells phases apart by parity only.
-        // Its last use may be the other warp's: once that is filled the use
-        // before it has been released, and the parity can mean one phase.
-        if (lane == 0) *my_next = op;
-        if (op >= C::kRing) {
-          if (!next_past(other_next, op - C::kRing)) alive = false;
-          if (alive) alive = mbar_wait(&empty[stage], (uint32_t)(op / C::kRing - 1) & 1u);
+        // use of the ring: 16 bits, the operand's place in the common order
+        const int use = kQ8 ? tile0 + j : op0 + (is_k ? op_of_k(j) : op_of_v(j, n));
+        const int ring = is_k ? C::kRingK : C::kRingV;
+        const int stage = use % ring;
+        if (!kQ8 && lane == 0) *my_next = use;
+        if (use >= ring) {
+          // The wait for the stage's release tells phases apart by parity only.
+          // In the common ring its last use may be the other warp's: once that
+          // is filled the use before it has been released, and the parity can
+          // mean one phase only.
+          if (!kQ8 && !next_past(other_next, use - ring)) alive = false;
+          if (alive) alive = mbar_wait(&empty[stage], (uint32_t)(use / ring - 1) & 1u);
         }
         const int sc = (tile0 + j) % kStepScales;
         if (alive && kQ8 && is_k && tile0 + j >= kStepScales)
@@ -264,7 +320,7 @@ __global__ void __launch_bounds__(step_threads<TC>(), 1)
         if (elect_one()) {
           mbar_arrive_expect_tx(&full[stage], (boxes << box_shift) * D * (int)sizeof(TC));
           if (kQ8 && is_k) mbar_arrive_expect_tx(&sm.scale_full[sc], (boxes << box_shift) * 8);
-          unsigned char* dst = kQ8 ? sm.raw[stage] : sm.op[stage];
+          unsigned char* dst = !kQ8 ? sm.op[stage] : is_k ? sm.in_k[stage] : sm.in_v[stage];
           const CUtensorMap* map = is_k ? &mk : &mv;
           constexpr int kWidth = kQ8 && D == 64 ? 64 : 128;
           constexpr int kHalves = kQ8 ? 1 : D / 64;
@@ -286,9 +342,10 @@ __global__ void __launch_bounds__(step_threads<TC>(), 1)
           }
         }
         __syncwarp();
-        if (is_k) sm.last_k = op;  // for the drain: the operands loaded last
-        else sm.last_v = op;
-        if (is_k) sm.last_tile = tile0 + j;
+        if (lane == 0) {  // for the drain after an abort
+          *(is_k ? &sm.last_k : &sm.last_v) = use;
+          if (is_k) sm.last_tile = tile0 + j;
+        }
       }
       op0 += 2 * n;
       tile0 += n;
@@ -298,49 +355,128 @@ __global__ void __launch_bounds__(step_threads<TC>(), 1)
     if (lane == 0 && is_k) parts.rec[blockIdx.x] = rec;
 
   } else if (warp == kStepLoadQ) {
-    // ---- loads: Q rows, K-major, 128-byte swizzle; rows behind the last are zero ----
+    // ---- Q rows to shared memory (rows behind the last are zero); V cleared
+    //      behind the end of a sequence ----
     bool alive = true;
+    int op0 = 0, n_before = 0;
+    Item before;
+    before.part = -1;
     for (int n_item = 0;; ++n_item) {
       const int slot = n_item % kStepItems, qb = n_item % C::kQBufs;
       alive = mbar_wait(&sm.item_full[slot], (uint32_t)(n_item / kStepItems) & 1u);
-      if (!__all_sync(0xffffffffu, alive)) break;
+      if (!__all_sync(0xffffffffu, alive)) {
+        alive = false;
+        break;
+      }
       const Item it = sm.item[slot];
       __syncwarp();
       if (lane == 0) mbar_arrive(&sm.item_empty[slot]);
-      if (it.part < 0) break;
-      if (n_item >= C::kQBufs)
-        alive = mbar_wait(&sm.q_empty[qb], (uint32_t)(n_item / C::kQBufs - 1) & 1u);
-      if (!__all_sync(0xffffffffu, alive)) break;
-      constexpr int kChunks = D / 8, kBatch = 8;
+      if (it.part >= 0) {
+        if (n_item >= C::kQBufs)
+          alive = mbar_wait(&sm.q_empty[qb], (uint32_t)(n_item / C::kQBufs - 1) & 1u);
+        if (!__all_sync(0xffffffffu, alive)) {
+          alive = false;
+          break;
+        }
+        constexpr int kChunks = D / 8, kBatch = kQ8 || N * D < 2048 ? 4 : 8;
+        static_assert(N * kChunks % (32 * kBatch) == 0, "whole batches");
 #pragma unroll 1
-      for (int i0 = lane; i0 < N * kChunks; i0 += 32 * kBatch) {
-        uint4 v[kBatch];
+        for (int i0 = lane; i0 < N * kChunks; i0 += 32 * kBatch) {
+          uint4 v[kBatch];
 #pragma unroll
-        for (int x = 0; x < kBatch; ++x) {
-          const int i = i0 + 32 * x, r = i / kChunks, c = i % kChunks;
-          v[x] = make_uint4(0, 0, 0, 0);
-          if (r < it.n_rows) {
-            const int rr = it.qt * N + r, tok = a.by_g.div(rr);
-            v[x] = *reinterpret_cast<const uint4*>(static_cast<const T*>(a.q) +
-                                                   (it.row0 + tok) * a.q_stride +
-                                                   (it.h * a.G + rr - tok * a.G) * D + 8 * c);
+          for (int x = 0; x < kBatch; ++x) {
+            const int i = i0 + 32 * x, r = i / kChunks, c = i % kChunks;
+            v[x] = make_uint4(0, 0, 0, 0);
+            if (r < it.n_rows) {
+              const int rr = it.qt * N + r, tok = a.by_g.div(rr);
+              v[x] = *reinterpret_cast<const uint4*>(static_cast<const T*>(a.q) +
+                                                     (it.row0 + tok) * a.q_stride +
+                                                     (it.h * a.G + rr - tok * a.G) * D + 8 * c);
+            }
+          }
+#pragma unroll
+          for (int x = 0; x < kBatch; ++x) {
+            const int i = i0 + 32 * x, r = i / kChunks, c = i % kChunks;
+            if constexpr (!kQ8) {
+              *reinterpret_cast<uint4*>(sm.q[qb] + sw128_offset(r, 8 * c, N)) = v[x];
+            } else {
+              // e4m3 parts of the row, scaled to a maximum in [128, 256)
+              float y[8], top = 0.0f;
+              unpack8<T>(v[x], y);
+#pragma unroll
+              for (int e = 0; e < 8; ++e) top = fmaxf(top, fabsf(y[e]));
+              bool odd = false;  // fmaxf passes over a NaN
+#pragma unroll
+              for (int e = 0; e < 8; ++e) odd |= !isfinite(y[e]);
+#pragma unroll
+              for (int w = kChunks / 2; w > 0; w >>= 1)
+                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, w));
+              const unsigned odds = __ballot_sync(0xffffffffu, odd);
+              const unsigned mine = (kChunks == 16 ? 0xffffu : 0xffu) << (lane / kChunks * kChunks);
+              int e2;
+              frexpf(top, &e2);
+              const int up = min(8 - e2, 120);  // top 2^up in [128, 256)
+              const float mul = ldexpf(1.0f, up);
+#pragma unroll
+              for (int e = 0; e < 8; ++e) y[e] *= mul;
+#pragma unroll
+              for (int pt = 0; pt < C::kQParts; ++pt) {
+                const uint32_t lo = f32_to_e4m3x4(y[0], y[1], y[2], y[3]);
+                const uint32_t hi = f32_to_e4m3x4(y[4], y[5], y[6], y[7]);
+                *reinterpret_cast<uint2*>(sm.q[qb] + pt * N * D + k8_offset<D>(r, 8 * c)) =
+                    make_uint2(lo, hi);
+                float z[8];
+                e4m3x4_to_f32(lo, z);
+                e4m3x4_to_f32(hi, z + 4);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) y[e] -= z[e];
+              }
+              // a row with a value that is not finite has no such parts: its
+              // results are not finite either way
+              if (c == 0) sm.qs[qb][r] = odds & mine ? CUDART_NAN_F : ldexpf(1.0f, -up);
+            }
           }
         }
-#pragma unroll
-        for (int x = 0; x < kBatch; ++x) {
-          const int i = i0 + 32 * x, r = i / kChunks, c = i % kChunks;
-          if (r < N) *reinterpret_cast<uint4*>(sm.q[qb] + sw128_offset(r, 8 * c, N)) = v[x];
-        }
+        fence_proxy_async_smem();
+        mbar_arrive(&sm.q_full[qb]);
       }
-      fence_proxy_async_smem();
-      mbar_arrive(&sm.q_full[qb]);
+      if (!kQ8 && before.part >= 0) {
+        // What lies behind the sequence in its last page may be anything, and 0
+        // times an infinity is none: clear those rows of the last V tile.  One
+        // item behind, so that Q of the next is there in time.
+        if (has_tail(before)) {
+          const int use = op0 + op_of_v(n_before - 1, n_before), os = use % C::kOps;
+          // once it is issued, the parity can mean this fill only
+          alive = next_past(&sm.next_v, use) &&
+                  mbar_wait(&sm.k_full[os], (uint32_t)(use / C::kOps) & 1u);
+          if (!__all_sync(0xffffffffu, alive)) {
+            alive = false;
+            break;
+          }
+          const int here = before.past + before.n - (before.t1 - 1) * kStepKeys;
+          for (int i = lane; i < (kStepKeys - here) * (D / 8); i += 32) {
+            const int k = here + i / (D / 8), c = i % (D / 8);
+            *reinterpret_cast<uint4*>(sm.op[os] + (c >> 3) * kStepKeys * 128 + k * 128 +
+                                      (c & 7) * 16) = make_uint4(0, 0, 0, 0);
+          }
+          fence_proxy_async_smem();
+        }
+        // (a slot of these can not be lapped: the next item in it is published
+        // when the MMA warp is past this one)
+        mbar_arrive(&sm.v_clean[(n_item - 1) % kStepItems]);
+        op0 += 2 * n_before;
+      }
+      if (it.part < 0) break;
+      before = it;
+      n_before = it.t1 - it.t0;
     }
     if (!alive) flags |= DSPARK_FLAG_TIMEOUT;
 
   } else if (warp == kStepMma) {
     // ---- MMA issue ----
-    constexpr uint32_t kIdS = idesc_tc<T>(128, N, false, false);
+    constexpr uint32_t kIdS = kQ8 ? idesc_e4m3(128, N) : idesc_tc<T>(128, N, false, false);
     constexpr uint32_t kIdO = idesc_tc<TP>(128, N, true, true);
+    constexpr uint32_t kIdL = idesc_tc<TP>(128, N, false, true);
     bool alive = true;
     int op0 = 0, tile0 = 0;
     for (int n_item = 0;; ++n_item) {
@@ -358,16 +494,29 @@ __global__ void __launch_bounds__(step_threads<TC>(), 1)
         alive = __all_sync(0xffffffffu, alive);
       };
       auto issue_s = [&](int j) {
-        const int op = op0 + op_of_k(j), os = op % C::kOps, buf = (tile0 + j) & 1;
-        wait(&sm.op_full[os], (uint32_t)(op / C::kOps) & 1u);
+        const int use = kQ8 ? tile0 + j : op0 + op_of_k(j), ks = use % C::kRingK;
+        const int buf = (tile0 + j) & 1;
+        wait(&sm.k_full[ks], (uint32_t)(use / C::kRingK) & 1u);
         tc_fence_after();
-        const uint64_t kd = sdesc_sw128(smem_u32(sm.op[os])), qd = sdesc_sw128(smem_u32(sm.q[qb]));
         if (alive && elect_one()) {
+          if constexpr (kQ8) {
+            const uint64_t kd = sdesc_k8<D>(smem_u32(sm.in_k[ks]));
+            const uint64_t qd = sdesc_k8<D>(smem_u32(sm.q[qb]));
 #pragma unroll
-          for (int k = 0; k < D / 16; ++k)
-            mma_bf16_ss(tmem + buf * N, kd + (((k >> 2) * kStepKeys * 128 + (k & 3) * 32) >> 4),
-                        qd + (((k >> 2) * N * 128 + (k & 3) * 32) >> 4), kIdS, k > 0);
-          mma_commit(&sm.op_empty[os]);
+            for (int pt = 0; pt < C::kQParts; ++pt)
+#pragma unroll
+              for (int k = 0; k < D / 32; ++k)
+                mma_e4m3_ss(tmem + buf * N, kd + ((k * 32) >> 4), qd + ((pt * N * D + k * 32) >> 4),
+                            kIdS, pt > 0 || k > 0);
+          } else {
+            const uint64_t kd = sdesc_sw128(smem_u32(sm.op[ks]));
+            const uint64_t qd = sdesc_sw128(smem_u32(sm.q[qb]));
+#pragma unroll
+            for (int k = 0; k < D / 16; ++k)
+              mma_bf16_ss(tmem + buf * N, kd + (((k >> 2) * kStepKeys * 128 + (k & 3) * 32) >> 4),
+                          qd + (((k >> 2) * N * 128 + (k & 3) * 32) >> 4), kIdS, k > 0);
+          }
+          mma_commit(&sm.k_empty[ks]);
           mma_commit(&sm.s_full[buf]);
           if (j == n - 1) mma_commit(&sm.q_empty[qb]);
         }
@@ -381,8 +530,9 @@ __global__ void __launch_bounds__(step_threads<TC>(), 1)
         wait(&sm.p_full[buf], (uint32_t)(g >> 1) & 1u);
         // the scores of tile j were read: their buffer takes those of j + 2
         if (j + 2 < n) issue_s(j + 2);
-        const int op = op0 + op_of_v(j, n), os = op % C::kOps;
-        wait(&sm.op_full[os], (uint32_t)(op / C::kOps) & 1u);
+        const int use = kQ8 ? g : op0 + op_of_v(j, n), os = use % C::kOps;
+        wait(kQ8 ? &sm.op_full[os] : &sm.k_full[os], (uint32_t)(use / C::kOps) & 1u);
+        if (!kQ8 && j == n - 1) wait(&sm.v_clean[slot], (uint32_t)(n_item / kStepItems) & 1u);
         tc_fence_after();
         // V: 64 elements of D in a row, 8 keys 1024 bytes apart, the other 64
         // behind all keys.  With D = 64 there are no others: lanes 64-127 of
@@ -390,12 +540,23 @@ __global__ void __launch_bounds__(step_threads<TC>(), 1)
         constexpr int kW = N < 64 ? N : 64;  // rows of P^T in a row of shared memory
         const uint64_t vd = sdesc_mn<64>(smem_u32(sm.op[os]), kStepKeys);
         const uint64_t pd = sdesc_mn<kW>(smem_u32(sm.p[buf]), kStepKeys);
+        const uint64_t od = sdesc_sw128(smem_u32(sm.ones));
         if (alive && elect_one()) {
 #pragma unroll
           for (int k = 0; k < kStepKeys / 16; ++k)
-            mma_bf16_ss(tmem + 2 * N, vd + ((k * 2048) >> 4), pd + ((k * 16 * kW * 2) >> 4), kIdO,
+            mma_bf16_ss(tmem + kColO, vd + ((k * 2048) >> 4), pd + ((k * 16 * kW * 2) >> 4), kIdO,
                         j > 0 || k > 0);
-          mma_commit(&sm.op_empty[os]);
+          mma_commit(kQ8 ? &sm.op_empty[os] : &sm.k_empty[os]);
+#pragma unroll
+          for (int k = 0; k < kStepKeys / 16; ++k) {
+            if constexpr (kQ8)
+              break;
+            else if constexpr (C::kOnesInTmem)
+              mma_bf16_ts(tmem + kColL, tmem + kColOnes, pd + ((k * 16 * kW * 2) >> 4), kIdL,
+                          j > 0 || k > 0);
+            else
+              mma_bf16_ss(tmem + kColL, od, pd + ((k * 16 * kW * 2) >> 4), kIdL, j > 0 || k > 0);
+          }
           mma_commit(&sm.p_empty[buf]);
         }
         __syncwarp();
@@ -409,11 +570,11 @@ __global__ void __launch_bounds__(step_threads<TC>(), 1)
     __syncwarp();
 
   } else if (warp >= kStepWiden) {
-    // ---- e4m3 tiles to 16 bits, in the operands' order ----
+    // ---- V tiles of e4m3 to bf16 ----
     if constexpr (kQ8) {
       const int tid = threadIdx.x - 32 * kStepWiden;
       bool alive = true;
-      int op = 0;
+      int use = 0;
       for (int n_item = 0;; ++n_item) {
         const int slot = n_item % kStepItems;
         if (alive) alive = mbar_wait(&sm.item_full[slot], (uint32_t)(n_item / kStepItems) & 1u);
@@ -425,21 +586,17 @@ __global__ void __launch_bounds__(step_threads<TC>(), 1)
         }
         if (tid == 0) mbar_arrive(&sm.item_empty[slot]);
         if (part < 0) break;
-        for (int s = 0; s < 2 * n && alive; ++s, ++op) {
-          const bool is_k = op_is_k(s, n);
-          const int rs = op % C::kRaws, os = op % C::kOps;
-          alive = mbar_wait(&sm.raw_full[rs], (uint32_t)(op / C::kRaws) & 1u);
-          if (alive && op >= C::kOps)
-            alive = mbar_wait(&sm.op_empty[os], (uint32_t)(op / C::kOps - 1) & 1u);
+        for (int j = 0; j < n && alive; ++j, ++use) {
+          const int vs = use % C::kRingV, os = use % C::kOps;
+          alive = mbar_wait(&sm.v_full[vs], (uint32_t)(use / C::kRingV) & 1u);
+          if (alive && use >= C::kOps)
+            alive = mbar_wait(&sm.op_empty[os], (uint32_t)(use / C::kOps - 1) & 1u);
           if (!alive) break;
-          if (is_k)
-            widen_tile<T, D>(sm.raw[rs], sm.op[os], tid);
-          else
-            widen_tile<__nv_bfloat16, D>(sm.raw[rs], sm.op[os], tid);
+          widen_tile<__nv_bfloat16, D>(sm.in_v[vs], sm.op[os], tid);
           fence_proxy_async_smem();
           __syncwarp();
           if (lane == 0) {
-            mbar_arrive(&sm.raw_empty[rs]);
+            mbar_arrive(&sm.v_empty[vs]);
             mbar_arrive(&sm.op_full[os]);
           }
         }
@@ -449,18 +606,25 @@ __global__ void __launch_bounds__(step_threads<TC>(), 1)
 
   } else {
     // ---- softmax: one key a thread, half of the rows a warpgroup ----
-    constexpr int R = N / 2;                  // rows of a thread
-    constexpr int kChunk32 = R < 32 ? R : 32; // columns of a load
-    constexpr int kLoads = R / kChunk32;
+    constexpr int R = N / 2;               // rows of a thread
+    constexpr int kCols = R == 64 && kQ8 ? 16 : R < 32 ? R : 32;  // columns of a load
+    constexpr int kLoads = R / kCols;
+    constexpr int kW = N < 64 ? N : 64;
     const int wg = warp >> 2, quarter = warp & 3;
-    const int key = quarter * 32 + lane;      // in the tile; in the epilogue: element of D
+    const int key = quarter * 32 + lane;   // in the tile; in the epilogue: element of D
     const int n0 = wg * R;
-    const uint32_t lane_base = (uint32_t)(quarter * 32) << 16;
+    const uint32_t lane_base = tmem + ((uint32_t)(quarter * 32) << 16);
     const int bar_wg = 2 + wg;
     bool alive = true;
-    int tile = 0, op0 = 0;
+    auto wait = [&](uint64_t* bar, uint32_t parity) {
+      if (alive && !mbar_wait_spin(bar, parity)) {
+        alive = false;
+        flags |= DSPARK_FLAG_TIMEOUT;
+      }
+    };
+    int tile = 0;
     for (int n_item = 0;; ++n_item) {
-      const int slot = n_item % kStepItems;
+      const int slot = n_item % kStepItems, qb = n_item % C::kQBufs;
       // one warp waits and says so to the others: all of them stop together
       if (warp == 0) {
         const bool ok = mbar_wait(&sm.item_full[slot], (uint32_t)(n_item / kStepItems) & 1u);
@@ -477,7 +641,7 @@ __global__ void __launch_bounds__(step_threads<TC>(), 1)
         sm.pos[n] = p;
         sm.low[n] = first_seen(p, a.window);
         sm.out[n] = ((it.row0 + tok) * a.Hq + it.h * a.G + rr - tok * a.G) * (long long)D;
-        sm.m[n] = n < it.n_rows ? -CUDART_INF_F : 0.0f;  // rows that pad: scores 0
+        sm.m[n] = 0.0f;
         sm.bad[n] = 0;
       }
       named_sync(1, 32 * kStepSoftmax);
@@ -485,23 +649,20 @@ __global__ void __launch_bounds__(step_threads<TC>(), 1)
       const int nt = it.t1 - it.t0;
       const int pos_min = it.past + a.by_g.div(it.qt * N);
       const int pos_max = it.past + a.by_g.div(it.qt * N + it.n_rows - 1);
-      float l[R];
+      const int low_max = first_seen(pos_max, a.window);
+      // e4m3: P carries V's scale, so its sums are not the weights': this
+      // thread's part of those
+      float l[kQ8 ? R : 1];
 #pragma unroll
-      for (int i = 0; i < R; ++i) l[i] = 0.0f;
+      for (int i = 0; i < (kQ8 ? R : 1); ++i) l[i] = 0.0f;
 
       for (int j = 0; j < nt; ++j, ++tile) {
         const int buf = tile & 1;
         const int k0 = (it.t0 + j) * kStepKeys;
         const int at = k0 + key;
-        const bool masked = k0 + kStepKeys > pos_min + 1 ||
-                            (a.window > 0 && k0 < pos_max - a.window + 1);
+        const bool masked = k0 + kStepKeys > pos_min + 1 || k0 < low_max;
+        const bool first = j == 0 || k0 <= low_max;  // the first keys of some row
         float kf = a.scale2, vs = 1.0f;
-        auto wait = [&](uint64_t* bar, uint32_t parity) {
-          if (alive && !mbar_wait_spin(bar, parity)) {
-            alive = false;
-            flags |= DSPARK_FLAG_TIMEOUT;
-          }
-        };
         if constexpr (kQ8) {
           const int sc = tile % kStepScales;
           wait(&sm.scale_full[sc], (uint32_t)(tile / kStepScales) & 1u);
@@ -513,22 +674,27 @@ __global__ void __launch_bounds__(step_threads<TC>(), 1)
         }
         wait(&sm.s_full[buf], (uint32_t)(tile >> 1) & 1u);
         tc_fence_after();
-        const uint32_t s_col = tmem + lane_base + buf * N + n0;
+        const uint32_t s_col = lane_base + buf * N + n0;
 
-        // scores over the reference, in units of log 2
-        float x[kChunk32];
-        auto load = [&](int c, bool over) {
-          uint32_t raw[kChunk32];
-          tmem_ld<kChunk32>(s_col + c * kChunk32, raw);
+        // scores of kCols rows from row c over the reference, in units of log 2
+        auto load = [&](auto& x, int c, bool over) {
+          constexpr int kX = sizeof(x) / 4;
+          uint32_t raw[kX];
+          tmem_ld<kX>(s_col + c, raw);
 #pragma unroll
-          for (int i = 0; i < kChunk32; i += 4) {
-            const int n = n0 + c * kChunk32 + i;
+          for (int i = 0; i < kX; i += 4) {
+            const int n = n0 + c + i;
             float4 m4 = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
             if (over) m4 = *reinterpret_cast<const float4*>(&sm.m[n]);
-            x[i] = fmaf(__uint_as_float(raw[i]), kf, -m4.x);
-            x[i + 1] = fmaf(__uint_as_float(raw[i + 1]), kf, -m4.y);
-            x[i + 2] = fmaf(__uint_as_float(raw[i + 2]), kf, -m4.z);
-            x[i + 3] = fmaf(__uint_as_float(raw[i + 3]), kf, -m4.w);
+            float4 f4 = make_float4(kf, kf, kf, kf);
+            if constexpr (kQ8) {
+              const float4 q4 = *reinterpret_cast<const float4*>(&sm.qs[qb][n]);
+              f4 = make_float4(kf * q4.x, kf * q4.y, kf * q4.z, kf * q4.w);
+            }
+            x[i] = fmaf(__uint_as_float(raw[i]), f4.x, -m4.x);
+            x[i + 1] = fmaf(__uint_as_float(raw[i + 1]), f4.y, -m4.y);
+            x[i + 2] = fmaf(__uint_as_float(raw[i + 2]), f4.z, -m4.z);
+            x[i + 3] = fmaf(__uint_as_float(raw[i + 3]), f4.w, -m4.w);
             if (masked) {
               const int4 p4 = *reinterpret_cast<const int4*>(&sm.pos[n]);
               const int4 l4 = *reinterpret_cast<const int4*>(&sm.low[n]);
@@ -539,153 +705,155 @@ __global__ void __launch_bounds__(step_threads<TC>(), 1)
             }
           }
         };
-        float top = -CUDART_INF_F;
+        float x[kCols];
+        bool hot = kHalfP && first;
+        {
+          float top = -CUDART_INF_F, bottom = CUDART_INF_F;
 #pragma unroll
-        for (int c = 0; c < kLoads; ++c) {
-          load(c, true);
+          for (int c = 0; c < R; c += kCols) {
+            load(x, c, true);
 #pragma unroll
-          for (int i = 0; i < kChunk32; ++i) top = fmaxf(top, x[i]);
+            for (int i = 0; i < kCols; ++i) top = fmaxf(top, x[i]);
+            if (!kHalfP && first) {
+#pragma unroll
+              for (int i = 0; i < kCols; ++i)
+                bottom = fminf(bottom, x[i] == -CUDART_INF_F ? CUDART_INF_F : x[i]);
+            }
+          }
+          hot |= top > kHot || bottom < -kHot;
         }
-        if (vote_any(bar_wg, 128, top > kHot)) {
-          // raise the references of this warpgroup's rows to the tile's maxima
+        if (vote_any(bar_wg, 128, hot)) {
+          // move the references of this warpgroup's rows to their maxima (loops
+          // kept short: this is rare, and its code should not crowd out the rest)
+#pragma unroll 1
+          for (int c = 0; c < R; c += 8) {
+            float y[8];
+            load(y, c, false);
 #pragma unroll
-          for (int c = 0; c < kLoads; ++c) {
-            load(c, false);
-#pragma unroll
-            for (int i = 0; i < kChunk32; ++i) {
-              const float w = warp_max_redux(x[i]);
-              if (lane == 0) sm.part[quarter][n0 + c * kChunk32 + i] = w;
+            for (int i = 0; i < 8; ++i) {
+              const float w = warp_max_redux(y[i]);
+              if (lane == 0) sm.part[quarter][n0 + c + i] = w;
             }
           }
           named_sync(bar_wg, 128);
           if (key < R) {
             const int n = n0 + key;
             const float old = sm.m[n];
-            float now = fmaxf(fmaxf(sm.part[0][n], sm.part[1][n]),
-                              fmaxf(sm.part[2][n], sm.part[3][n]));
-            if (n >= it.n_rows) now = 0.0f;
-            now = fmaxf(now, old);
-            sm.f[n] = old == now || old == -CUDART_INF_F ? (old == now ? 1.0f : 0.0f) : ex2(old - now);
+            const float top = fmaxf(fmaxf(sm.part[0][n], sm.part[1][n]),
+                                    fmaxf(sm.part[2][n], sm.part[3][n]));
+            const bool seen = j > 0 && k0 > sm.low[n];  // has keys before this tile
+            const float now = seen ? fmaxf(old, top) : top == -CUDART_INF_F ? old : top;
+            sm.f[n] = seen && now != old ? ex2(old - now) : 1.0f;
             sm.m[n] = now;
           }
           named_sync(bar_wg, 128);
+          if constexpr (kQ8) {
+#pragma unroll
+            for (int i = 0; i < R; ++i) l[i] *= sm.f[n0 + i];
+          }
           if (j > 0) {
-            wait(&sm.p_empty[buf ^ 1], (uint32_t)((tile - 1) >> 1) & 1u);  // O^T of tile j - 1
+            wait(&sm.p_empty[buf ^ 1], (uint32_t)((tile - 1) >> 1) & 1u);  // O^T, L of tile j - 1
             tc_fence_after();
-          }
+#pragma unroll 1
+            for (int c = 0; c < (kQ8 ? R : 2 * R); c += 8) {  // O^T, then L
+              const int n = n0 + (c < R ? c : c - R);
+              const uint32_t col = lane_base + (c < R ? kColO : kColL) + n;
+              uint32_t o[8];
+              tmem_ld<8>(col, o);
 #pragma unroll
-          for (int c = 0; c < kLoads; ++c) {
-            uint32_t o[kChunk32];
-            const uint32_t col = tmem + lane_base + 2 * N + n0 + c * kChunk32;
-            if (j > 0) tmem_ld<kChunk32>(col, o);
-#pragma unroll
-            for (int i = 0; i < kChunk32; ++i) {
-              const float f = sm.f[n0 + c * kChunk32 + i];
-              l[c * kChunk32 + i] *= f;
-              if (j > 0) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
+              for (int i = 0; i < 8; ++i)
+                o[i] = __float_as_uint(__uint_as_float(o[i]) * sm.f[n + i]);
+              tmem_st<8>(col, o);
             }
-            if (j > 0) tmem_st<kChunk32>(col, o);
+            tmem_st_wait();
           }
-          if (j > 0) tmem_st_wait();
-          if (kLoads == 1) load(0, true);
+          if (kLoads == 1) load(x, 0, true);
         }
         // weights; the buffer was last read by the MMAs of tile - 2
         if (tile >= 2) wait(&sm.p_empty[buf], (uint32_t)((tile >> 1) - 1) & 1u);
         unsigned char* prow = sm.p[buf];
 #pragma unroll
-        for (int c = 0; c < kLoads; ++c) {
-          if (kLoads > 1) load(c, true);
+        for (int c = 0; c < R; c += kCols) {
+          if (kLoads > 1) load(x, c, true);
 #pragma unroll
-          for (int i = 0; i < kChunk32; i += 8) {
+          for (int i = 0; i < kCols; i += 8) {
             uint32_t w[4];
 #pragma unroll
             for (int y = 0; y < 8; y += 2) {
               float p0 = ex2(x[i + y]), p1 = ex2(x[i + y + 1]);
-              l[c * kChunk32 + i + y] += p0;
-              l[c * kChunk32 + i + y + 1] += p1;
-              if constexpr (kQ8) {  // a masked position's scale may be anything
+              if constexpr (kQ8) {
+                l[c + i + y] += p0;
+                l[c + i + y + 1] += p1;
+                // a masked position's scale may be anything
                 p0 = x[i + y] == -CUDART_INF_F ? 0.0f : p0 * vs;
                 p1 = x[i + y + 1] == -CUDART_INF_F ? 0.0f : p1 * vs;
               }
               w[y / 2] = Pair<TP>::put(p0, p1);
             }
-            *reinterpret_cast<uint4*>(prow + mn_offset<(N < 64 ? N : 64)>(
-                                                 n0 + c * kChunk32 + i, key, kStepKeys)) =
+            *reinterpret_cast<uint4*>(prow + mn_offset<kW>(n0 + c + i, key, kStepKeys)) =
                 make_uint4(w[0], w[1], w[2], w[3]);
           }
         }
-        if (!kQ8 && wg == 0 && it.past + it.n - k0 < kStepKeys) {
-          // what lies behind the sequence in its last page may be anything, and
-          // 0 times an infinity is none: clear those rows of V
-          const int op = op0 + op_of_v(j, nt), os = op % C::kOps;
-          wait(&sm.op_full[os], (uint32_t)(op / C::kOps) & 1u);
-          if (at >= it.past + it.n) {
-#pragma unroll
-            for (int c = 0; c < D / 8; ++c)
-              *reinterpret_cast<uint4*>(sm.op[os] + (c >> 3) * kStepKeys * 128 + key * 128 +
-                                        (c & 7) * 16) = make_uint4(0, 0, 0, 0);
-          }
-        }
+        (void)vs;
         fence_proxy_async_smem();
         tc_fence_before();
         mbar_arrive(&sm.p_full[buf]);
       }
-      op0 += 2 * nt;
+      if (kQ8) {
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sm.q_empty[qb]);  // qs is read
+      }
 
-      // ---- the item's sums and results ----
-#pragma unroll
-      for (int c = 0; c < R; c += kChunk32) {
-        // sums over the warp's 32 keys: halves of the rows to halves of the lanes
-        float v[kChunk32];
-#pragma unroll
-        for (int i = 0; i < kChunk32; ++i) v[i] = l[c + i];
-        const float s = lanes_reduce<kChunk32>(v, lane);
-        if (lane < kChunk32) sm.part[quarter][n0 + c + lane] = s;
-      }
-      auto wait = [&](uint64_t* bar, uint32_t parity) {
-        if (alive && !mbar_wait_spin(bar, parity)) {
-          alive = false;
-          flags |= DSPARK_FLAG_TIMEOUT;
-        }
-      };
-      named_sync(bar_wg, 128);
-      const bool whole = it.part == 0;
-      const size_t slot_row = (size_t)(2 * blockIdx.x + (it.part == 2)) * N;
-      if (key < R) {
-        const int n = n0 + key;
-        const float L = (sm.part[0][n] + sm.part[1][n]) + (sm.part[2][n] + sm.part[3][n]);
-        sm.f[n] = 1.0f / L;
-        if (!whole && n < it.n_rows) parts.ml[slot_row + n] = make_float2(sm.m[n], L);
-      }
+      // ---- the item's results: O^T and L of all its keys ----
       wait(&sm.p_empty[(tile - 1) & 1], (uint32_t)((tile - 1) >> 1) & 1u);
       tc_fence_after();
-      named_sync(bar_wg, 128);
-      if (key < D) {  // uniform over a warp
+      const bool whole = it.part == 0;
+      const size_t slot_row = (size_t)(2 * blockIdx.x + (it.part == 2)) * N;
+      bool bad = false;
+      if constexpr (kQ8) {
+        // the 128 threads' sums, through the P buffers (their MMAs are done)
+        float* ls = reinterpret_cast<float*>(sm.p) + n0 * kStepKeys;
 #pragma unroll
-        for (int c = 0; c < R; c += 8) {
-          if (n0 + c >= it.n_rows) break;
-          uint32_t o[8];
-          tmem_ld<8>(tmem + lane_base + 2 * N + n0 + c, o);
+        for (int i = 0; i < R; ++i) ls[i * kStepKeys + key] = l[i];
+        named_sync(bar_wg, 128);
+        constexpr int kPer = 128 / R;  // threads that sum a row
+        const int r = key / kPer;
+        float s = 0.0f;
+#pragma unroll 8
+        for (int i = key % kPer; i < kStepKeys; i += kPer) s += ls[r * kStepKeys + i];
+#pragma unroll
+        for (int w = kPer / 2; w > 0; w >>= 1) s += __shfl_xor_sync(0xffffffffu, s, w);
+        if (key % kPer == 0) sm.f[n0 + r] = s;
+        named_sync(bar_wg, 128);
+      }
+      if (key < D) {  // uniform over a warp
+#pragma unroll 1
+        for (int c = 0; c < R && n0 + c < it.n_rows; c += 8) {
+          uint32_t o[8], L8[8];
+          tmem_ld<8>(lane_base + kColO + n0 + c, o);
+          if constexpr (!kQ8) tmem_ld<8>(lane_base + kColL + n0 + c, L8);
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
             const int n = n0 + c + i;
-            if (n < it.n_rows) {
-              if (whole) {
-                const float v = __uint_as_float(o[i]) * sm.f[n];
-                if (!isfinite(v)) sm.bad[n] = 1;
-                static_cast<T*>(a.out)[sm.out[n] + key] = to_elem<T>(v);
-              } else {
-                parts.o[(slot_row + n) * D + key] = __uint_as_float(o[i]);
-              }
+            if (n >= it.n_rows) break;
+            const float v = __uint_as_float(o[i]);
+            const float L = kQ8 ? sm.f[n] : __uint_as_float(L8[i]);
+            if (whole) {
+              const float r = v / L;
+              if (!isfinite(r)) sm.bad[n] = bad = true;
+              static_cast<T*>(a.out)[sm.out[n] + key] = to_elem<T>(r);
+            } else {
+              parts.o[(slot_row + n) * D + key] = v;
+              if (key == 0)  // a part without a visible key has no reference
+                parts.ml[slot_row + n] = make_float2(L == 0.0f ? -CUDART_INF_F : sm.m[n], L);
             }
           }
         }
       }
       tc_fence_before();
-      named_sync(bar_wg, 128);
       // a result that is not finite may come from a position that its row does
       // not see (0 times infinity): form the row again from those it sees
-      if (whole) {
+      if (vote_any(bar_wg, 128, bad)) {
         for (int n = n0 + quarter; n < n0 + R && n < it.n_rows; n += 4) {
           if (!sm.bad[n]) continue;
           const int rr = it.qt * N + n, tok = a.by_g.div(rr);
@@ -702,17 +870,19 @@ __global__ void __launch_bounds__(step_threads<TC>(), 1)
   // after an abort copies may still be in flight: none outlives the CTA
   if (sm.flags & DSPARK_FLAG_TIMEOUT) {
     if (threadIdx.x == 0) {
-      uint64_t* full = kQ8 ? sm.raw_full : sm.op_full;
-      const int last = max(sm.last_k, sm.last_v);
-      for (int op = max(last - C::kRing + 1, 0); op <= last; ++op)
-        mbar_wait(&full[op % C::kRing], (uint32_t)(op / C::kRing) & 1u);
-      if (kQ8)
+      const int last_k = kQ8 ? sm.last_k : max(sm.last_k, sm.last_v);
+      for (int u = max(last_k - C::kRingK + 1, 0); u <= last_k; ++u)
+        mbar_wait(&sm.k_full[u % C::kRingK], (uint32_t)(u / C::kRingK) & 1u);
+      if (kQ8) {
+        for (int u = max(sm.last_v - C::kRingV + 1, 0); u <= sm.last_v; ++u)
+          mbar_wait(&sm.v_full[u % C::kRingV], (uint32_t)(u / C::kRingV) & 1u);
         for (int t = max(sm.last_tile - kStepScales + 1, 0); t <= sm.last_tile; ++t)
           mbar_wait(&sm.scale_full[t % kStepScales], (uint32_t)(t / kStepScales) & 1u);
+      }
     }
     __syncthreads();
   }
-  if (warp == kStepMma) tmem_dealloc(tmem, kTmemCols);
+  if (warp == kStepMma) tmem_dealloc(tmem, C::kTmemCols);
   if (threadIdx.x == 0) store_status(a.status, sm.flags);
 }
 

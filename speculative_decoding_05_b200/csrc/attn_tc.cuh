@@ -97,6 +97,39 @@ __device__ __forceinline__ void tmem_st(uint32_t addr, const uint32_t (&r)[C]) {
   }
 }
 
+// Descriptors of the kind::f8f6f4 MMA, e4m3 x e4m3 -> fp32, 32 elements of K an
+// instruction, both operands K-major with rows of W bytes (128 or 64), swizzled
+// over the row.
+__host__ __device__ constexpr uint32_t idesc_e4m3(int M, int N) {
+  return (1u << 4) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
+}
+template <int W>
+__device__ __forceinline__ uint64_t sdesc_k8(uint32_t addr) {
+  static_assert(W == 128 || W == 64, "row width");
+  uint64_t d = 0;
+  d |= (uint64_t)((addr & 0x3FFFFu) >> 4);
+  d |= (uint64_t)1 << 16;
+  d |= (uint64_t)((8 * W) >> 4) << 32;
+  d |= (uint64_t)1 << 46;
+  d |= (uint64_t)(W == 128 ? 2 : 4) << 61;
+  return d;
+}
+__device__ __forceinline__ void mma_e4m3_ss(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc,
+                                            uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+// Byte offset of byte b of row r in rows of W bytes, swizzled over the row.
+template <int W>
+__device__ __forceinline__ uint32_t k8_offset(int r, int b) {
+  const int sw = W == 128 ? (r & 7) : ((r >> 1) & 3);
+  return (uint32_t)(r * W + (((b >> 4) ^ sw) << 4) + (b & 15));
+}
+
 // Whether `p` holds for any of the `count` threads at named barrier `id`.
 __device__ __forceinline__ bool vote_any(int id, int count, bool p) {
   uint32_t r;
@@ -115,25 +148,6 @@ __device__ __forceinline__ float warp_max_redux(float v) {
   float r;
   asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
   return r;
-}
-
-// Sums of v[i] over the warp, that of v[i] in the lanes that are i modulo C: at
-// each step a lane keeps half of its values and adds the other lane's.
-template <int C>
-__device__ __forceinline__ float lanes_reduce(float (&v)[C], int lane) {
-#pragma unroll
-  for (int w = C / 2; w > 0; w >>= 1) {
-    const bool up = lane & w;
-#pragma unroll
-    for (int i = 0; i < w; ++i) {
-      const float keep = up ? v[i + w] : v[i], give = up ? v[i] : v[i + w];
-      v[i] = keep + __shfl_xor_sync(0xffffffffu, give, w);
-    }
-  }
-  float s = v[0];
-#pragma unroll
-  for (int w = C; w < 32; w <<= 1) s += __shfl_xor_sync(0xffffffffu, s, w);
-  return s;
 }
 
 template <typename T>
@@ -167,25 +181,33 @@ __device__ __forceinline__ uint32_t widen2(uint32_t x) {
 // threads.
 template <typename T, int D>
 __device__ __forceinline__ void widen_tile(const unsigned char* raw, unsigned char* op, int tid) {
-  constexpr int kChunks = D / 16;
-#pragma unroll 4
-  for (int i = tid; i < 128 * kChunks; i += 128) {
-    const int row = i / kChunks, c = i % kChunks;
-    const uint4 u = *reinterpret_cast<const uint4*>(
-        raw + (D == 64 ? row * 64 + ((c ^ ((row >> 1) & 3)) << 4)
-                       : row * 128 + ((c ^ (row & 7)) << 4)));
-    uint4 o[2];
-    o[0] = make_uint4(widen2<T>(__byte_perm(u.x, 0, 0x1404)), widen2<T>(__byte_perm(u.x, 0, 0x3424)),
-                      widen2<T>(__byte_perm(u.y, 0, 0x1404)), widen2<T>(__byte_perm(u.y, 0, 0x3424)));
-    o[1] = make_uint4(widen2<T>(__byte_perm(u.z, 0, 0x1404)), widen2<T>(__byte_perm(u.z, 0, 0x3424)),
-                      widen2<T>(__byte_perm(u.w, 0, 0x1404)), widen2<T>(__byte_perm(u.w, 0, 0x3424)));
-    // the halves of D lie on the same banks: their lanes store in opposite order
+  constexpr int kChunks = D / 16, kBatch = 4;
 #pragma unroll
-    for (int x = 0; x < 2; ++x) {
-      const int y = x ^ (c >> 2);
-      const int oc = 2 * c + y;
-      *reinterpret_cast<uint4*>(op + (oc >> 3) * 128 * 128 + row * 128 +
-                                (((oc & 7) ^ (row & 7)) << 4)) = y ? o[1] : o[0];
+  for (int i0 = tid; i0 < 128 * kChunks; i0 += 128 * kBatch) {
+    uint4 u[kBatch];
+#pragma unroll
+    for (int b = 0; b < kBatch; ++b) {
+      const int i = i0 + 128 * b;
+      u[b] = *reinterpret_cast<const uint4*>(raw + k8_offset<D>(i / kChunks, i % kChunks * 16));
+    }
+#pragma unroll
+    for (int b = 0; b < kBatch; ++b) {
+      const int i = i0 + 128 * b, row = i / kChunks, c = i % kChunks;
+      uint4 o[2];
+      o[0] = make_uint4(
+          widen2<T>(__byte_perm(u[b].x, 0, 0x1404)), widen2<T>(__byte_perm(u[b].x, 0, 0x3424)),
+          widen2<T>(__byte_perm(u[b].y, 0, 0x1404)), widen2<T>(__byte_perm(u[b].y, 0, 0x3424)));
+      o[1] = make_uint4(
+          widen2<T>(__byte_perm(u[b].z, 0, 0x1404)), widen2<T>(__byte_perm(u[b].z, 0, 0x3424)),
+          widen2<T>(__byte_perm(u[b].w, 0, 0x1404)), widen2<T>(__byte_perm(u[b].w, 0, 0x3424)));
+      // the halves of D lie on the same banks: their lanes store in opposite order
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        const int y = x ^ (c >> 2);
+        const int oc = 2 * c + y;
+        *reinterpret_cast<uint4*>(op + (oc >> 3) * 128 * 128 + row * 128 +
+                                  (((oc & 7) ^ (row & 7)) << 4)) = y ? o[1] : o[0];
+      }
     }
   }
 }

@@ -211,7 +211,7 @@ struct LaunchAttn {
 
   template <typename T, typename TC, int Dh, int N>
   dspark_status step() const {
-    constexpr int smem = (int)sizeof(StepSmem<TC, Dh, N>) + 1024;
+    constexpr int smem = (int)sizeof(StepSmem<T, TC, Dh, N>) + 1024;
     static_assert(smem <= kSmemLimit, "shared memory");
     static DeviceOnce once;
     set_smem_once(once, attn_step_kernel<T, TC, Dh, N>, smem);
