@@ -134,7 +134,7 @@ size_t dspark_attn_workspace_size(int B, int Hq, int Hkv, int D, int max_len);
  *   out[row, h, :] = sum_j w_j V_j,  w = softmax_j(sm_scale * q[row, h] . K_j)
  *   over max(0, i - window + 1) <= j <= i   (window = 0: over all j <= i)
  * Scores, softmax statistics and sums are fp32; the weights are rounded to 16
- * bits (the value rows' type; bf16 with an e4m3 cache) for the product with
+ * bits (the value rows' type; fp16 with an e4m3 cache) for the product with
  * V; out is rounded once.  Positions a row does not see never reach it: K and
  * V there may hold anything, infinities and NaN included.
  *

@@ -14,6 +14,8 @@
 // results do not depend on timing.
 #pragma once
 
+#include <type_traits>
+
 #include "attn_rows.cuh"
 #include "tc_common.cuh"
 
@@ -251,81 +253,98 @@ __host__ inline PartBytes part_bytes(int ctas, int rows, int D) {
 }
 
 constexpr int kJoinThreads = 256;
+constexpr int kMaxAttnCtas = 256;
 
-// Joins the parts of the item that CTA blockIdx.x began: out = sum_i 2^(m_i - M)
-// o_i / sum_i 2^(m_i - M) l_i over the parts in the order of their keys.
-// blockIdx.y takes every gridDim.y-th group of rows.
+// Joins the parts of split items: out = sum_i 2^(m_i - M) o_i / sum_i
+// 2^(m_i - M) l_i over an item's parts in the order of their keys: slot 1 of the
+// CTA that began it, then slot 0 of the CTAs behind it up to the one that ends
+// it.  A warp a row; the rows of all split items are one line, dealt out over
+// all warps (few items have many rows and parts, many have few).
 template <typename T, typename TC, int D>
 __global__ void __launch_bounds__(kJoinThreads)
-    attn_join_kernel(const AttnArgs a, const AttnTiles t, const AttnParts p, int ctas) {
-  constexpr int kLanes = D / 4;               // threads of a row, 4 elements each
-  constexpr int kRows = kJoinThreads / kLanes;
-  __shared__ int s_parts[kMaxStatusCtas];
-  __shared__ int s_n;
-  __shared__ int s_bad[kRows];
+    attn_join_kernel(const AttnArgs a, const int tile_rows, const AttnParts p, const int ctas) {
+  constexpr int E = D / 32;  // elements of a lane
+  using V = typename std::conditional<E == 4, float4, float2>::type;
+  __shared__ int s_head[kMaxAttnCtas], s_first[kMaxAttnCtas + 1], s_warp[kJoinThreads / 32];
+  static_assert(kMaxAttnCtas <= kJoinThreads, "a record a thread");
   grid_dep_wait();
-  const int c0 = blockIdx.x;
-  const PartRecord rec = p.rec[c0];
-  if (rec.b < 0) return;
-  // the parts: slot 1 of c0, then slot 0 of the CTAs behind it up to the one
-  // that ends the item (32 records at a time)
-  if (threadIdx.x < 32) {
-    int n = 0;
-    for (int c = c0 + 1; c < ctas; c += 32) {
-      const int head = c + threadIdx.x < ctas ? p.rec[c + threadIdx.x].head : 0;
-      const unsigned ends = __ballot_sync(0xffffffffu, head == 1);
-      const unsigned upto = ends ? (2u << (__ffs(ends) - 1)) - 1u : 0xffffffffu;
-      const unsigned in = __ballot_sync(0xffffffffu, head != 0) & upto;
-      if (in >> threadIdx.x & 1)
-        s_parts[n + __popc(in & ((1u << threadIdx.x) - 1u))] = 2 * (c + threadIdx.x);
-      n += __popc(in);
-      if (ends) break;
-    }
-    if (threadIdx.x == 0) s_n = n;
-  }
-  __syncthreads();
-  const int n = s_n;
-  const int lane = threadIdx.x % kLanes, rg = threadIdx.x / kLanes;
-  for (int r0 = blockIdx.y * kRows; r0 < rec.n_rows; r0 += gridDim.y * kRows) {
-    const int r = r0 + rg;
-    if (lane == 0) s_bad[rg] = 0;
-    __syncthreads();
-    if (r < rec.n_rows) {
-      const size_t first = (size_t)(2 * c0 + 1) * t.rows + r;
-      float M = p.ml[first].x;
-      for (int i = 0; i < n; ++i) M = fmaxf(M, p.ml[(size_t)s_parts[i] * t.rows + r].x);
-      const float Mu = M == -CUDART_INF_F ? 0.0f : M;
-      float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-      float L = 0.0f;
-#pragma unroll 4
-      for (int i = -1; i < n; ++i) {
-        const size_t at = i < 0 ? first : (size_t)s_parts[i] * t.rows + r;
-        const float2 ml = p.ml[at];
-        const float4 v = *reinterpret_cast<const float4*>(p.o + at * D + 4 * lane);
-        const float w = exp2f(ml.x - Mu);
-        L = fmaf(w, ml.y, L);
-        o.x = fmaf(w, v.x, o.x); o.y = fmaf(w, v.y, o.y);
-        o.z = fmaf(w, v.z, o.z); o.w = fmaf(w, v.w, o.w);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  scan_requests<kJoinThreads>(ctas, s_first, s_warp, [&](int c) {
+    s_head[c] = p.rec[c].head;
+    return p.rec[c].b >= 0 ? p.rec[c].n_rows : 0;
+  });
+  const int total = s_first[ctas];
+  constexpr int kWarps = kJoinThreads / 32;
+  for (int i = blockIdx.x * kWarps + warp; i < total; i += gridDim.x * kWarps) {
+    const int c0 = find_request(s_first, ctas, i);
+    const int r = i - s_first[c0];
+    const PartRecord rec = p.rec[c0];
+    float o[E], M = -CUDART_INF_F, L = 0.0f;
+#pragma unroll
+    for (int e = 0; e < E; ++e) o[e] = 0.0f;
+    // parts in batches, so that their loads overlap
+    constexpr int kBatch = 8;
+    int c = c0;
+    bool more = true;
+    while (more) {
+      float2 ml[kBatch];
+      V v[kBatch];
+#pragma unroll
+      for (int k = 0; k < kBatch; ++k) {
+        int slot = -1;
+        if (more) {
+          if (c > c0)
+            while (c < ctas - 1 && s_head[c] == 0) ++c;  // CTAs without keys of this item
+          slot = c == c0 ? 2 * c + 1 : 2 * c;
+          more = c < ctas - 1 && (c == c0 || s_head[c] == 2);
+          ++c;
+        }
+        ml[k] = make_float2(-CUDART_INF_F, 0.0f);
+        v[k] = V{};
+        if (slot >= 0) {
+          const size_t at = (size_t)slot * tile_rows + r;
+          ml[k] = p.ml[at];
+          v[k] = *reinterpret_cast<const V*>(p.o + at * D + lane * E);
+        }
       }
-      const float inv = 1.0f / L;
-      o.x *= inv; o.y *= inv; o.z *= inv; o.w *= inv;
-      if (!isfinite(o.x) || !isfinite(o.y) || !isfinite(o.z) || !isfinite(o.w)) s_bad[rg] = 1;
-      const int rr = rec.qt * t.rows + r, tok = a.by_g.div(rr);
-      T* dst = static_cast<T*>(a.out) +
-               ((rec.row0 + tok) * a.Hq + rec.h * a.G + rr - tok * a.G) * D + 4 * lane;
-      *reinterpret_cast<uint2*>(dst) = make_uint2(Pair<T>::put(o.x, o.y), Pair<T>::put(o.z, o.w));
+      float Mn = M;
+#pragma unroll
+      for (int k = 0; k < kBatch; ++k) Mn = fmaxf(Mn, ml[k].x);
+      const float Mu = Mn == -CUDART_INF_F ? 0.0f : Mn;
+      const float back = exp2f(M - Mu);
+      L *= back;
+#pragma unroll
+      for (int e = 0; e < E; ++e) o[e] *= back;
+#pragma unroll
+      for (int k = 0; k < kBatch; ++k) {
+        const float w = exp2f(ml[k].x - Mu);
+        L = fmaf(w, ml[k].y, L);
+        const float* x = reinterpret_cast<const float*>(&v[k]);
+#pragma unroll
+        for (int e = 0; e < E; ++e) o[e] = fmaf(w, x[e], o[e]);
+      }
+      M = Mn;
     }
-    __syncthreads();
-    // a result that is not finite may come from a position that its row does
-    // not see (0 times infinity): form the row again from those it sees
-    for (int k = threadIdx.x / 32; k < kRows; k += kJoinThreads / 32) {
-      if (!s_bad[k]) continue;
-      const int rr = rec.qt * t.rows + r0 + k, tok = a.by_g.div(rr);
+    const float inv = 1.0f / L;
+    bool odd = false;
+#pragma unroll
+    for (int e = 0; e < E; ++e) {
+      o[e] *= inv;
+      odd |= !isfinite(o[e]);
+    }
+    const int rr = rec.qt * tile_rows + r, tok = a.by_g.div(rr);
+    const int hq = rec.h * a.G + rr - tok * a.G;
+    if (__any_sync(0xffffffffu, odd)) {
+      // a result that is not finite may come from a position that its row does
+      // not see (0 times infinity): form the row again from those it sees
       unsigned flags = 0;
-      attend_row<T, TC, D>(a, rec.b, rec.past + tok, rec.h * a.G + rr - tok * a.G, rec.row0 + tok,
-                           flags);
+      attend_row<T, TC, D>(a, rec.b, rec.past + tok, hq, rec.row0 + tok, flags);
+    } else {
+      T* dst = static_cast<T*>(a.out) + ((rec.row0 + tok) * a.Hq + hq) * D + lane * E;
+#pragma unroll
+      for (int e = 0; e < E; e += 2)
+        *reinterpret_cast<uint32_t*>(dst + e) = Pair<T>::put(o[e], o[e + 1]);
     }
-    __syncthreads();
   }
 }
 
@@ -337,14 +356,5 @@ __global__ void __launch_bounds__(kJoinThreads)
 // bytes (64 where an e4m3 row has no more), swizzled over that width.
 bool encode_cache_map(CUtensorMap* m, const void* cache, int D, bool is_e4m3, bool is_f16,
                       long long rows, int box_rows);
-
-// Byte offset of 16-byte chunk c of key row k in a tile of `keys` keys.
-template <typename TC, int D>
-__device__ __forceinline__ uint32_t tile_offset(int keys, int k, int c) {
-  if constexpr (sizeof(TC) == 1 && D == 64)
-    return (uint32_t)(k * 64 + ((c ^ ((k >> 1) & 3)) << 4));
-  else
-    return (uint32_t)((c >> 3) * keys * 128 + k * 128 + (((c & 7) ^ (k & 7)) << 4));
-}
 
 }  // namespace dspark

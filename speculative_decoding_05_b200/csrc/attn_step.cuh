@@ -25,8 +25,9 @@
 // rounded again (4 more).  bf16 has 8 and fp16 11 bits, so the sum is exact for
 // elements down to 2^-9 (2^-6) of the row's maximum; below that it is off by at
 // most 2^-17 of the maximum, less than what bf16 itself (2^-8 of the element)
-// rounds off a row of such a spread.  K's scale is applied to the scores.  P is
-// bf16 with V's scale on it, so V's codes are widened, by 4 warps.
+// rounds off a row of such a spread.  K's scale is applied to the scores.  V's
+// codes are widened to fp16 (exact) by 4 warps, and P is fp16 with V's scale on
+// it: the reference is such that the product stays in fp16's range.
 //
 // Warps: 8 softmax, one each that loads K (and walks the piece), V and Q, one
 // that issues the MMAs, 4 that widen V (e4m3).  The operands pass in the order
@@ -149,7 +150,7 @@ __global__ void __launch_bounds__(step_threads<TC>(), 1)
                      const __grid_constant__ CUtensorMap mv, const int box_shift) {
   using C = StepCfg<T, TC, D, N>;
   using S = StepSmem<T, TC, D, N>;
-  using TP = typename std::conditional<C::kQ8, __nv_bfloat16, T>::type;  // P and V
+  using TP = typename std::conditional<C::kQ8, __half, T>::type;  // P and V
   constexpr bool kQ8 = C::kQ8;
   constexpr int kThreads = step_threads<TC>();
   constexpr int kColO = 2 * N, kColL = 3 * N, kColOnes = 4 * N;  // TMEM: S^T twice, O^T, L, ones
@@ -378,10 +379,22 @@ __global__ void __launch_bounds__(step_threads<TC>(), 1)
           alive = false;
           break;
         }
-        constexpr int kChunks = D / 8, kBatch = kQ8 || N * D < 2048 ? 4 : 8;
+        constexpr int kChunks = D / 8, kBatch = N * D < 2048 ? 4 : 8;
         static_assert(N * kChunks % (32 * kBatch) == 0, "whole batches");
+        if constexpr (!kQ8) {
+#pragma unroll 8
+          for (int i = lane; i < N * kChunks; i += 32) {
+            const int r = i / kChunks, c = i % kChunks;
+            const int rr = it.qt * N + min(r, it.n_rows - 1), tok = a.by_g.div(rr);
+            cp_async16(sm.q[qb] + sw128_offset(r, 8 * c, N),
+                       static_cast<const T*>(a.q) + (it.row0 + tok) * a.q_stride +
+                           (it.h * a.G + rr - tok * a.G) * D + 8 * c,
+                       r < it.n_rows);
+          }
+          cp_async_wait_all();
+        }
 #pragma unroll 1
-        for (int i0 = lane; i0 < N * kChunks; i0 += 32 * kBatch) {
+        for (int i0 = kQ8 ? lane : N * kChunks; i0 < N * kChunks; i0 += 32 * kBatch) {
           uint4 v[kBatch];
 #pragma unroll
           for (int x = 0; x < kBatch; ++x) {
@@ -397,9 +410,7 @@ __global__ void __launch_bounds__(step_threads<TC>(), 1)
 #pragma unroll
           for (int x = 0; x < kBatch; ++x) {
             const int i = i0 + 32 * x, r = i / kChunks, c = i % kChunks;
-            if constexpr (!kQ8) {
-              *reinterpret_cast<uint4*>(sm.q[qb] + sw128_offset(r, 8 * c, N)) = v[x];
-            } else {
+            if constexpr (kQ8) {
               // e4m3 parts of the row, scaled to a maximum in [128, 256)
               float y[8], top = 0.0f;
               unpack8<T>(v[x], y);
@@ -570,7 +581,7 @@ __global__ void __launch_bounds__(step_threads<TC>(), 1)
     __syncwarp();
 
   } else if (warp >= kStepWiden) {
-    // ---- V tiles of e4m3 to bf16 ----
+    // ---- V tiles of e4m3 to fp16 ----
     if constexpr (kQ8) {
       const int tid = threadIdx.x - 32 * kStepWiden;
       bool alive = true;
@@ -592,7 +603,7 @@ __global__ void __launch_bounds__(step_threads<TC>(), 1)
           if (alive && use >= C::kOps)
             alive = mbar_wait(&sm.op_empty[os], (uint32_t)(use / C::kOps - 1) & 1u);
           if (!alive) break;
-          widen_tile<__nv_bfloat16, D>(sm.in_v[vs], sm.op[os], tid);
+          widen_tile<D>(sm.in_v[vs], sm.op[os], tid);
           fence_proxy_async_smem();
           __syncwarp();
           if (lane == 0) {
@@ -662,13 +673,14 @@ __global__ void __launch_bounds__(step_threads<TC>(), 1)
         const int at = k0 + key;
         const bool masked = k0 + kStepKeys > pos_min + 1 || k0 < low_max;
         const bool first = j == 0 || k0 <= low_max;  // the first keys of some row
-        float kf = a.scale2, vs = 1.0f;
+        float kf = a.scale2, vs = 1.0f, vs2 = 0.0f;
         if constexpr (kQ8) {
           const int sc = tile % kStepScales;
           wait(&sm.scale_full[sc], (uint32_t)(tile / kStepScales) & 1u);
           kf *= sm.scale[sc][0][key];
           vs = sm.scale[sc][1][key];
           consumed(kf + vs);
+          vs2 = fmaxf(__log2f(vs), -60.0f);  // P carries the scale: its size counts
           __syncwarp();
           if (lane == 0) mbar_arrive(&sm.scale_empty[sc]);
         }
@@ -720,7 +732,7 @@ __global__ void __launch_bounds__(step_threads<TC>(), 1)
                 bottom = fminf(bottom, x[i] == -CUDART_INF_F ? CUDART_INF_F : x[i]);
             }
           }
-          hot |= top > kHot || bottom < -kHot;
+          hot |= top + vs2 > kHot || bottom < -kHot;
         }
         if (vote_any(bar_wg, 128, hot)) {
           // move the references of this warpgroup's rows to their maxima (loops
@@ -731,7 +743,7 @@ __global__ void __launch_bounds__(step_threads<TC>(), 1)
             load(y, c, false);
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-              const float w = warp_max_redux(y[i]);
+              const float w = warp_max_redux(y[i] + vs2);
               if (lane == 0) sm.part[quarter][n0 + c + i] = w;
             }
           }
@@ -827,25 +839,39 @@ __global__ void __launch_bounds__(step_threads<TC>(), 1)
         named_sync(bar_wg, 128);
       }
       if (key < D) {  // uniform over a warp
+        // e4m3: V was widened with the elements of four in the order 0 2 1 3
+        const int d = kQ8 ? (key & ~3) | (key & 1) << 1 | (key >> 1 & 1) : key;
+        const int last = min(n0 + R, it.n_rows);
 #pragma unroll 1
-        for (int c = 0; c < R && n0 + c < it.n_rows; c += 8) {
+        for (int n = n0; n < last; n += 8) {
           uint32_t o[8], L8[8];
-          tmem_ld<8>(lane_base + kColO + n0 + c, o);
-          if constexpr (!kQ8) tmem_ld<8>(lane_base + kColL + n0 + c, L8);
+          tmem_ld8_issue(lane_base + kColO + n, o);
+          if constexpr (!kQ8) tmem_ld8_issue(lane_base + kColL + n, L8);
+          tmem_ld8_wait(o);
+          if constexpr (!kQ8) tmem_ld8_wait(L8);
+          float L[8];
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const int n = n0 + c + i;
-            if (n >= it.n_rows) break;
-            const float v = __uint_as_float(o[i]);
-            const float L = kQ8 ? sm.f[n] : __uint_as_float(L8[i]);
-            if (whole) {
-              const float r = v / L;
-              if (!isfinite(r)) sm.bad[n] = bad = true;
-              static_cast<T*>(a.out)[sm.out[n] + key] = to_elem<T>(r);
-            } else {
-              parts.o[(slot_row + n) * D + key] = v;
-              if (key == 0)  // a part without a visible key has no reference
-                parts.ml[slot_row + n] = make_float2(L == 0.0f ? -CUDART_INF_F : sm.m[n], L);
+          for (int i = 0; i < 8; ++i) L[i] = kQ8 ? sm.f[n + i] : __uint_as_float(L8[i]);
+          if (whole) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              const float r = __uint_as_float(o[i]) * __frcp_rn(L[i]);
+              if (n + i < last) {
+                static_cast<T*>(a.out)[sm.out[n + i] + d] = to_elem<T>(r);
+                if (!isfinite(r)) sm.bad[n + i] = bad = true;
+              }
+            }
+          } else {
+            float* dst = parts.o + (slot_row + n) * D + d;
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+              if (n + i < last) dst[i * D] = __uint_as_float(o[i]);
+            if (key == 0) {  // a part without a visible key has no reference
+#pragma unroll
+              for (int i = 0; i < 8; ++i)
+                if (n + i < last)
+                  parts.ml[slot_row + n + i] =
+                      make_float2(L[i] == 0.0f ? -CUDART_INF_F : sm.m[n + i], L[i]);
             }
           }
         }

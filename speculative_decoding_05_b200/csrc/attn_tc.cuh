@@ -57,6 +57,20 @@ __device__ __forceinline__ bool elect_one() {
   return r != 0;
 }
 
+// 8 columns, split as tmem_ld32_issue / tmem_ld32_wait.
+__device__ __forceinline__ void tmem_ld8_issue(uint32_t addr, uint32_t (&r)[8]) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]),
+                 "=r"(r[6]), "=r"(r[7])
+               : "r"(addr));
+}
+__device__ __forceinline__ void tmem_ld8_wait(uint32_t (&r)[8]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]),
+                 "+r"(r[6]), "+r"(r[7])
+               :
+               : "memory");
+}
 template <int C>
 __device__ __forceinline__ void tmem_ld(uint32_t addr, uint32_t (&r)[C]) {
   static_assert(C == 8 || C == 16 || C == 32, "columns");
@@ -67,13 +81,8 @@ __device__ __forceinline__ void tmem_ld(uint32_t addr, uint32_t (&r)[C]) {
     tmem_ld16_issue(addr, r);
     tmem_ld16_wait(r);
   } else {
-    asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];\n\t"
-        "tcgen05.wait::ld.sync.aligned;"
-        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
-          "=r"(r[7])
-        : "r"(addr)
-        : "memory");
+    tmem_ld8_issue(addr, r);
+    tmem_ld8_wait(r);
   }
 }
 template <int C>
@@ -156,58 +165,55 @@ __device__ __forceinline__ T to_elem(float v) {
   else return __float2bfloat16_rn(v);
 }
 
-// Two e4m3 codes, in the high bytes of the halves of x (low bytes 0), as 16-bit
-// values: the four exponent bits land on the low exponent bits of the wider
-// type (subnormal codes on its subnormals), and a power of two makes up for
-// the difference of the biases: 2^(127 - 7) for bf16, 2^(15 - 7) for fp16.
-// Both steps are exact.
-template <typename T>
-__device__ __forceinline__ uint32_t widen2(uint32_t x) {
-  if constexpr (std::is_same<T, __half>::value) {
-    const uint32_t y = (x & 0x80008000u) | ((x >> 1) & 0x3f803f80u);
-    const __half2 r = __hmul2(*reinterpret_cast<const __half2*>(&y), __floats2half2_rn(256.0f, 256.0f));
-    return *reinterpret_cast<const uint32_t*>(&r);
-  } else {
-    const uint32_t y = (x & 0x80008000u) | ((x >> 4) & 0x07f007f0u);
-    const uint32_t two120 = 0x7b807b80u;
-    const __nv_bfloat162 r = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&y),
-                                     *reinterpret_cast<const __nv_bfloat162*>(&two120));
-    return *reinterpret_cast<const uint32_t*>(&r);
-  }
+// 16 bytes from global to shared memory without registers; zeros if !take.
+__device__ __forceinline__ void cp_async16(void* dst, const void* src, bool take) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(dst)), "l"(src),
+               "r"(take ? 16 : 0)
+               : "memory");
+}
+__device__ __forceinline__ void cp_async_wait_all() {
+  asm volatile("cp.async.wait_all;" ::: "memory");
 }
 
-// An e4m3 tile of 128 rows x D bytes (as TMA wrote it, swizzled over its row)
-// to T in the operands' layout (64-element halves, 128-byte swizzle), by 128
-// threads.
-template <typename T, int D>
+// Four e4m3 codes as fp16, the pairs (0, 2) and (1, 3) (exact).  A code in the
+// high byte of a half is s eeee mmm; shifted right by one behind its sign the
+// exponent lands on the low four of fp16's five bits (subnormal codes on its
+// subnormals), and 2^8 makes up for the difference of the biases, 15 - 7.
+__device__ __forceinline__ uint2 widen4(uint32_t c) {
+  const uint32_t even = ((c << 7) & 0x3f803f80u) | ((c << 8) & 0x80008000u);
+  const uint32_t odd = ((c >> 1) & 0x3f803f80u) | (c & 0x80008000u);
+  const __half2 f = __floats2half2_rn(256.0f, 256.0f);
+  const __half2 x = __hmul2(*reinterpret_cast<const __half2*>(&even), f);
+  const __half2 y = __hmul2(*reinterpret_cast<const __half2*>(&odd), f);
+  return make_uint2(*reinterpret_cast<const uint32_t*>(&x), *reinterpret_cast<const uint32_t*>(&y));
+}
+
+// An e4m3 tile of 128 rows x D bytes (as TMA wrote it, swizzled over its row) to
+// fp16 in the operands' layout (64-element halves, 128-byte swizzle), by 128
+// threads; elements of four in the order 0 2 1 3.
+template <int D>
 __device__ __forceinline__ void widen_tile(const unsigned char* raw, unsigned char* op, int tid) {
   constexpr int kChunks = D / 16, kBatch = 4;
+  const int c = tid % kChunks;
+  // the halves of D lie on the same banks: their lanes take the two halves of
+  // their 16 bytes in opposite order
+  const bool swap = c & 4;
 #pragma unroll
   for (int i0 = tid; i0 < 128 * kChunks; i0 += 128 * kBatch) {
     uint4 u[kBatch];
 #pragma unroll
-    for (int b = 0; b < kBatch; ++b) {
-      const int i = i0 + 128 * b;
-      u[b] = *reinterpret_cast<const uint4*>(raw + k8_offset<D>(i / kChunks, i % kChunks * 16));
-    }
+    for (int b = 0; b < kBatch; ++b)
+      u[b] = *reinterpret_cast<const uint4*>(raw + k8_offset<D>((i0 + 128 * b) / kChunks, 16 * c));
 #pragma unroll
     for (int b = 0; b < kBatch; ++b) {
-      const int i = i0 + 128 * b, row = i / kChunks, c = i % kChunks;
-      uint4 o[2];
-      o[0] = make_uint4(
-          widen2<T>(__byte_perm(u[b].x, 0, 0x1404)), widen2<T>(__byte_perm(u[b].x, 0, 0x3424)),
-          widen2<T>(__byte_perm(u[b].y, 0, 0x1404)), widen2<T>(__byte_perm(u[b].y, 0, 0x3424)));
-      o[1] = make_uint4(
-          widen2<T>(__byte_perm(u[b].z, 0, 0x1404)), widen2<T>(__byte_perm(u[b].z, 0, 0x3424)),
-          widen2<T>(__byte_perm(u[b].w, 0, 0x1404)), widen2<T>(__byte_perm(u[b].w, 0, 0x3424)));
-      // the halves of D lie on the same banks: their lanes store in opposite order
-#pragma unroll
-      for (int x = 0; x < 2; ++x) {
-        const int y = x ^ (c >> 2);
-        const int oc = 2 * c + y;
-        *reinterpret_cast<uint4*>(op + (oc >> 3) * 128 * 128 + row * 128 +
-                                  (((oc & 7) ^ (row & 7)) << 4)) = y ? o[1] : o[0];
-      }
+      const int row = (i0 + 128 * b) / kChunks;
+      unsigned char* dst = op + (c >> 2) * 128 * 128 + row * 128;
+      const uint2 a0 = widen4(swap ? u[b].z : u[b].x), a1 = widen4(swap ? u[b].w : u[b].y);
+      *reinterpret_cast<uint4*>(dst + ((((2 * c + swap) & 7) ^ (row & 7)) << 4)) =
+          make_uint4(a0.x, a0.y, a1.x, a1.y);
+      const uint2 b0 = widen4(swap ? u[b].x : u[b].z), b1 = widen4(swap ? u[b].y : u[b].w);
+      *reinterpret_cast<uint4*>(dst + ((((2 * c + !swap) & 7) ^ (row & 7)) << 4)) =
+          make_uint4(b0.x, b0.y, b1.x, b1.y);
     }
   }
 }

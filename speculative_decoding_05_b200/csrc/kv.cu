@@ -8,7 +8,6 @@
 #include <cstdint>
 #include <type_traits>
 
-#include "attn_split.cuh"
 #include "attn_step.cuh"
 #include "kv_common.cuh"
 #include "kv_rows.cuh"
@@ -155,9 +154,10 @@ struct LaunchRead {
   }
 };
 
-// CTAs of the attention kernels: the partial results of a workspace have room
-// for two CTAs on each of a B200's SMs.
+// CTAs of the attention kernels, one an SM: the partial results of a workspace
+// have room for a B200's.
 constexpr int kAttnMaxSms = 148;
+static_assert(kAttnMaxSms <= kMaxAttnCtas && kAttnMaxSms <= kMaxStatusCtas, "records");
 int attn_sms() { return kv_sms() < kAttnMaxSms ? kv_sms() : kAttnMaxSms; }
 
 struct LaunchAttn {
@@ -186,27 +186,9 @@ struct LaunchAttn {
   }
 
   template <typename T, typename TC, int Dh>
-  dspark_status join(const AttnTiles& t, const AttnParts& p, int ctas) const {
-    const int groups = (t.rows * (Dh / 4) + kJoinThreads - 1) / kJoinThreads;
-    return launched(launch_dependent(attn_join_kernel<T, TC, Dh>, dim3(ctas, groups < 4 ? groups : 4),
-                                     dim3(kJoinThreads), 0, s, a, t, p, ctas));
-  }
-
-  template <typename T, typename TC, int Dh, int MT>
-  dspark_status split() const {
-    constexpr int smem = (int)sizeof(SplitSmem<TC, Dh, MT>) + 1024;
-    static DeviceOnce once;
-    set_smem_once(once, attn_split_kernel<T, TC, Dh, MT>, smem);
-    const int ctas = 2 * attn_sms();
-    const AttnTiles t = {16 * MT, split_keys<TC, Dh>()};
-    const AttnParts p = parts(ctas, t.rows);
-    CUtensorMap mk, mv;
-    int box;
-    if (!maps<T, TC>(&mk, &mv, t.keys, &box)) return DSPARK_ERR_CUDA;
-    const dspark_status st = launched(launch_dependent(attn_split_kernel<T, TC, Dh, MT>, dim3(ctas),
-                                                       dim3(kSplitThreads), smem, s, a, p, mk, mv,
-                                                       box));
-    return st != DSPARK_OK ? st : join<T, TC, Dh>(t, p, ctas);
+  dspark_status join(int tile_rows, const AttnParts& p, int ctas) const {
+    return launched(launch_dependent(attn_join_kernel<T, TC, Dh>, dim3(2 * attn_sms()),
+                                     dim3(kJoinThreads), 0, s, a, tile_rows, p, ctas));
   }
 
   template <typename T, typename TC, int Dh, int N>
@@ -216,17 +198,16 @@ struct LaunchAttn {
     static DeviceOnce once;
     set_smem_once(once, attn_step_kernel<T, TC, Dh, N>, smem);
     const int ctas = attn_sms();
-    const AttnTiles t = {N, kStepKeys};
-    const AttnParts p = parts(ctas, t.rows);
+    const AttnParts p = parts(ctas, N);
     CUtensorMap mk, mv;
     int box;
-    if (!maps<T, TC>(&mk, &mv, t.keys, &box)) return DSPARK_ERR_CUDA;
+    if (!maps<T, TC>(&mk, &mv, kStepKeys, &box)) return DSPARK_ERR_CUDA;
     int box_shift = 0;
     while (1 << box_shift < box) ++box_shift;
     const dspark_status st = launched(launch_dependent(attn_step_kernel<T, TC, Dh, N>, dim3(ctas),
                                                        dim3(step_threads<TC>()), smem, s, a, p, mk,
                                                        mv, box_shift));
-    return st != DSPARK_OK ? st : join<T, TC, Dh>(t, p, ctas);
+    return st != DSPARK_OK ? st : join<T, TC, Dh>(N, p, ctas);
   }
 
   template <typename T, typename TC, int Dh>

@@ -108,9 +108,14 @@ def attention(p, sm_scale=None, window=0):
     score is a fp32 sum of D products (error at most D 2^-23 S, S the largest
     sum of |q k| scale) scaled and turned into 2^x (relative 2^-21 and, of
     |score| <= S, 2^-22 S), which moves weight and normaliser: twice.  Then
-    one rounding of the result."""
+    one rounding of the result.
+
+    e4m3: the weights are fp16 with V's scale on them, the largest such product
+    at least 1, so half the smallest step is against max|v| again.  Queries are
+    sums of e4m3 parts, off by at most 2^-17 of the row's largest element each:
+    a score by 2^-17 max|q| sum|k| scale."""
     sm_scale = p.D ** -0.5 if sm_scale is None else sm_scale
-    u_p = half_step(torch.bfloat16 if p.cache != torch.float16 else torch.float16)
+    u_p = half_step(torch.bfloat16 if p.cache == torch.bfloat16 else torch.float16)
     u_o = half_step(p.act)
     res = []
     for b in range(len(p.new)):
@@ -143,9 +148,14 @@ def attention(p, sm_scale=None, window=0):
                 bad = torch.where(finite[j], torch.zeros_like(vz[j]), vz[j])
                 o[rows] = o[rows] + bad
             A = w @ va.abs()
-            eps = u_p + L * 2.0 ** -23 + 2 * (p.D * 2.0 ** -23 * S + 2.0 ** -21 + 2.0 ** -22 * S)
+            if p.cache == torch.float8_e4m3fn:
+                part = 2.0 ** -17 * sm_scale * q[:, h].abs().amax(-1, True) * kh.abs().sum(-1)
+                S8 = part.masked_fill(~seen, 0).amax(-1, True)
+            else:
+                S8 = 0.0
+            eps = 2 * S8 + u_p + L * 2.0 ** -23 + 2 * (p.D * 2.0 ** -23 * S + 2.0 ** -21 + 2.0 ** -22 * S)
             t = A * eps
-            if p.cache == torch.float16:
+            if p.cache != torch.bfloat16:
                 t = t + L * 2.0 ** -25 * va.abs().amax()
             out[:, h] = o
             tol[:, h] = t + u_o * (o.abs() + t) + 1e-30
