@@ -1,5 +1,5 @@
 // attn_step.cuh -- attention of a decode or verify step on the tensor cores:
-// up to 128 (token, query head) rows an item.
+// up to 80 (token, query head) rows an item.
 //
 // The cache's bytes bound such a call as long as the work on a key stays
 // short.  The warp-level matrix instructions do not keep up: 32 padded rows
@@ -11,7 +11,11 @@
 //                                       [128 keys][N rows] written by the threads
 //   L   [., N rows]      += 1 P^T       the weights' sums, alike in every lane
 //                                       (e4m3: summed by the threads)
-// A thread owns one key and N / 2 rows of S^T (two warpgroups share the rows).
+// Two pairs of warpgroups take the tiles in turn, each with O^T and L of its
+// own, joined at the item's end: a tile's softmax is a chain of some 2000 clocks
+// (scores out of TMEM, exponentials, weights to shared memory, hand-over to the
+// MMAs), the stream brings a tile in 1400 to 2800.  A thread owns one key and
+// half of the N rows.
 // A row's softmax then lies across threads, so its reference is not the running
 // maximum: weights are 2^(s - m) with m = 0 to begin with, which costs no
 // precision in floating point while scores stay within 2^+-kHot, and one vote a
@@ -29,7 +33,7 @@
 // codes are widened to fp16 (exact) by 4 warps, and P is fp16 with V's scale on
 // it: the reference is such that the product stays in fp16's range.
 //
-// Warps: 8 softmax, one each that loads K (and walks the piece), V and Q, one
+// Warps: 16 softmax, one each that loads K (and walks the piece), V and Q, one
 // that issues the MMAs, 4 that widen V (e4m3).  The operands pass in the order
 // K0 K1 K2 V0 K3 V1 ..: scores are formed two tiles ahead, as far as their two
 // buffers reach.
@@ -43,7 +47,7 @@
 namespace dspark {
 
 constexpr int kStepKeys = 128;
-constexpr int kStepSoftmax = 8;                    // warps
+constexpr int kStepSoftmax = 16;                   // warps, in two streams of two groups
 constexpr int kStepLoadK = kStepSoftmax;           // warp
 constexpr int kStepLoadV = kStepSoftmax + 1;       // warp
 constexpr int kStepLoadQ = kStepSoftmax + 2;       // warp
@@ -69,15 +73,15 @@ struct StepCfg {
   static constexpr int kTileIn = kStepKeys * D * (int)sizeof(TC);  // a tile as TMA brings it
   static constexpr int kQBufs = N <= 64 ? 2 : 1;
   static constexpr int kQBytes = N * D * (kQ8 ? kQParts : 2);
+  static constexpr int kW = N % 64 == 0 ? 64 : N % 32 == 0 ? 32 : 16;  // rows of P^T in a line
   static constexpr int kPBytes = kStepKeys * N * 2;
-  // the MMA of L (16 bits) takes its ones from TMEM while that has room for them
-  static constexpr bool kOnesInTmem = !kQ8 && N <= 64;
-  static constexpr int kOnes = kQ8 || kOnesInTmem ? 0 : kStepKeys * 128;
-  // S^T twice, O^T, L, ones; without the last two: 3 N, to a power of two
-  static constexpr int kTmemCols = kQ8 ? (N <= 64 ? 4 * N : 512) : N <= 16 ? 128 : N <= 32 ? 256 : 512;
+  // TMEM: S^T, O^T and L (16 bits) for each stream, the ones that make L
+  static constexpr int kCols = kQ8 ? 4 * N : 6 * N + 8;
+  static constexpr int kTmemCols = kCols <= 64 ? 64 : kCols <= 128 ? 128 : kCols <= 256 ? 256 : 512;
+  static_assert(kCols <= 512, "TMEM");
   static constexpr int kSmall = 10240;
   // 16 KB behind the 16-bit tiles, see StepSmem
-  static constexpr int kPQ = kQBufs * kQBytes + 2 * kPBytes + kOnes;
+  static constexpr int kPQ = kQBufs * kQBytes + 2 * kPBytes;
   static constexpr int kBehind = kPQ < 16384 ? 16384 - kPQ : 16;
   static constexpr int kLeft = kSmemLimit - 1024 - kSmall - kPQ - kBehind;
   static constexpr int kOps = kQ8 ? 2 : kLeft / kTile < 8 ? kLeft / kTile : 8;
@@ -92,18 +96,17 @@ template <typename T, typename TC, int D, int N>
 struct StepSmem {
   using C = StepCfg<T, TC, D, N>;
   alignas(1024) unsigned char op[C::kOps][C::kTile];
-  // with D = 64 the MMAs of V read 16 KB past a tile (see the MMA warp): p, q,
-  // ones and `behind` are as much
+  // with D = 64 the MMAs of V read 16 KB past a tile (see the MMA warp): p, q
+  // and `behind` are as much
   alignas(1024) unsigned char p[2][C::kPBytes];
   alignas(1024) unsigned char q[C::kQBufs][C::kQBytes];
-  alignas(1024) unsigned char ones[C::kOnes ? C::kOnes : 16];
   unsigned char behind[C::kBehind];
   alignas(1024) unsigned char in_k[C::kQ8 ? C::kRingK : 1][C::kQ8 ? C::kTileIn : 16];
   alignas(1024) unsigned char in_v[C::kQ8 ? C::kRingV : 1][C::kQ8 ? C::kTileIn : 16];
   float scale[C::kQ8 ? kStepScales : 1][2][kStepKeys];
-  float qs[C::kQBufs][N];           // e4m3: power of two that was taken off a row of Q
-  float m[N], f[N], part[4][N];
-  int pos[N], low[N], bad[N];
+  alignas(16) float qs[C::kQBufs][N];         // e4m3: power of two that was taken off a row of Q
+  alignas(16) float m[2][N], f[2][N], part[2][4][N];  // of each stream
+  int low[N], bad[N];
   long long out[N];
   uint64_t k_full[C::kRingK], k_empty[C::kRingK];  // 16 bits: of the common ring
   uint64_t v_full[C::kRingV], v_empty[C::kRingV];  // e4m3 only, as the next
@@ -116,7 +119,7 @@ struct StepSmem {
   uint64_t drain;
   Item item[kStepItems];
   Piece piece;
-  long long scan[16];
+  long long scan[24];
   uint32_t tmem;
   unsigned flags;
   int stop;
@@ -153,7 +156,7 @@ __global__ void __launch_bounds__(step_threads<TC>(), 1)
   using TP = typename std::conditional<C::kQ8, __half, T>::type;  // P and V
   constexpr bool kQ8 = C::kQ8;
   constexpr int kThreads = step_threads<TC>();
-  constexpr int kColO = 2 * N, kColL = 3 * N, kColOnes = 4 * N;  // TMEM: S^T twice, O^T, L, ones
+  constexpr int kColO = 2 * N, kColL = 4 * N, kColOnes = 6 * N;  // TMEM: see StepCfg
   constexpr bool kHalfP = std::is_same<TP, __half>::value;
   // Scores this far over the reference move it: 2^64 leaves fp32 sums and bf16
   // weights far from their ends, 2^14 fp16 ones.  At the first keys of a row a
@@ -180,13 +183,13 @@ __global__ void __launch_bounds__(step_threads<TC>(), 1)
     }
     for (int i = 0; i < kStepScales; ++i) {
       mbar_init(&sm.scale_full[i], 1);
-      mbar_init(&sm.scale_empty[i], kStepSoftmax);
+      mbar_init(&sm.scale_empty[i], kStepSoftmax / 2);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&sm.q_full[i], 32);
       mbar_init(&sm.q_empty[i], kQ8 ? 1 + kStepSoftmax : 1);
       mbar_init(&sm.s_full[i], 1);
-      mbar_init(&sm.p_full[i], 32 * kStepSoftmax);
+      mbar_init(&sm.p_full[i], 32 * kStepSoftmax / 2);
       mbar_init(&sm.p_empty[i], 1);
     }
     for (int i = 0; i < kStepItems; ++i) {
@@ -202,18 +205,13 @@ __global__ void __launch_bounds__(step_threads<TC>(), 1)
   }
   if (warp == kStepMma) tmem_alloc(&sm.tmem, C::kTmemCols);
   constexpr uint32_t kOne2 = kHalfP ? 0x3c003c00u : 0x3f803f80u;
-  if constexpr (C::kOnes > 0) {
-    for (int i = threadIdx.x; i < C::kOnes / 16; i += kThreads)
-      reinterpret_cast<uint4*>(sm.ones)[i] = make_uint4(kOne2, kOne2, kOne2, kOne2);
-    fence_proxy_async_smem();
-  }
   grid_dep_launch();
   grid_dep_wait();
   tc_fence_before();
   find_piece<kThreads>(a, tiles, sm.scan, &sm.piece, flags);  // syncs the block
   tc_fence_after();
   const uint32_t tmem = sm.tmem;
-  if constexpr (C::kOnesInTmem) {
+  if constexpr (!kQ8) {
     if (warp < 4) {
       uint32_t o[8];
 #pragma unroll
@@ -380,7 +378,7 @@ __global__ void __launch_bounds__(step_threads<TC>(), 1)
           break;
         }
         constexpr int kChunks = D / 8, kBatch = N * D < 2048 ? 4 : 8;
-        static_assert(N * kChunks % (32 * kBatch) == 0, "whole batches");
+        static_assert(!kQ8 || N * kChunks % (32 * kBatch) == 0, "whole batches");
         if constexpr (!kQ8) {
 #pragma unroll 8
           for (int i = lane; i < N * kChunks; i += 32) {
@@ -548,25 +546,20 @@ __global__ void __launch_bounds__(step_threads<TC>(), 1)
         // V: 64 elements of D in a row, 8 keys 1024 bytes apart, the other 64
         // behind all keys.  With D = 64 there are no others: lanes 64-127 of
         // O^T take what lies there and nobody reads them.
-        constexpr int kW = N < 64 ? N : 64;  // rows of P^T in a row of shared memory
+        constexpr int kW = C::kW;
         const uint64_t vd = sdesc_mn<64>(smem_u32(sm.op[os]), kStepKeys);
         const uint64_t pd = sdesc_mn<kW>(smem_u32(sm.p[buf]), kStepKeys);
-        const uint64_t od = sdesc_sw128(smem_u32(sm.ones));
         if (alive && elect_one()) {
 #pragma unroll
           for (int k = 0; k < kStepKeys / 16; ++k)
-            mma_bf16_ss(tmem + kColO, vd + ((k * 2048) >> 4), pd + ((k * 16 * kW * 2) >> 4), kIdO,
-                        j > 0 || k > 0);
+            mma_bf16_ss(tmem + kColO + buf * N, vd + ((k * 2048) >> 4),
+                        pd + ((k * 16 * kW * 2) >> 4), kIdO, j > 1 || k > 0);
           mma_commit(kQ8 ? &sm.op_empty[os] : &sm.k_empty[os]);
+          if constexpr (!kQ8) {
 #pragma unroll
-          for (int k = 0; k < kStepKeys / 16; ++k) {
-            if constexpr (kQ8)
-              break;
-            else if constexpr (C::kOnesInTmem)
-              mma_bf16_ts(tmem + kColL, tmem + kColOnes, pd + ((k * 16 * kW * 2) >> 4), kIdL,
-                          j > 0 || k > 0);
-            else
-              mma_bf16_ss(tmem + kColL, od, pd + ((k * 16 * kW * 2) >> 4), kIdL, j > 0 || k > 0);
+            for (int k = 0; k < kStepKeys / 16; ++k)
+              mma_bf16_ts(tmem + kColL + buf * N, tmem + kColOnes, pd + ((k * 16 * kW * 2) >> 4),
+                          kIdL, j > 1 || k > 0);
           }
           mma_commit(&sm.p_empty[buf]);
         }
@@ -591,7 +584,7 @@ __global__ void __launch_bounds__(step_threads<TC>(), 1)
         if (alive) alive = mbar_wait(&sm.item_full[slot], (uint32_t)(n_item / kStepItems) & 1u);
         const int part = sm.item[slot].part, n = sm.item[slot].t1 - sm.item[slot].t0;
         // all four warps go on or all stop
-        if (vote_any(4, 128, !alive)) {
+        if (vote_any(6, 128, !alive)) {
           alive = false;
           break;
         }
@@ -616,24 +609,27 @@ __global__ void __launch_bounds__(step_threads<TC>(), 1)
     }
 
   } else {
-    // ---- softmax: one key a thread, half of the rows a warpgroup ----
-    constexpr int R = N / 2;               // rows of a thread
-    constexpr int kCols = R == 64 && kQ8 ? 16 : R < 32 ? R : 32;  // columns of a load
+    // ---- softmax: the streams take the tiles in turn, a thread one key ----
+    constexpr int R = N / 2;                      // rows of a thread
+    constexpr int kCols = R % 16 == 0 ? 16 : 8;   // columns of a load
     constexpr int kLoads = R / kCols;
-    constexpr int kW = N < 64 ? N : 64;
+    constexpr int kW = C::kW;
+    // e4m3: P carries V's scale, so its sums are not the weights': those are
+    // summed by the threads, when the vote has let the tile pass
+    constexpr bool kKeep = kQ8 && kLoads == 1;    // a tile's weights are kept until then
     const int wg = warp >> 2, quarter = warp & 3;
-    const int key = quarter * 32 + lane;   // in the tile; in the epilogue: element of D
-    const int n0 = wg * R;
+    const int stream = wg >> 1, n0 = (wg & 1) * R;
+    const int key = quarter * 32 + lane;          // in the tile; in the epilogue: lane of O^T
     const uint32_t lane_base = tmem + ((uint32_t)(quarter * 32) << 16);
     const int bar_wg = 2 + wg;
     bool alive = true;
     auto wait = [&](uint64_t* bar, uint32_t parity) {
-      if (alive && !mbar_wait_spin(bar, parity)) {
+      if (alive && !mbar_wait(bar, parity)) {
         alive = false;
         flags |= DSPARK_FLAG_TIMEOUT;
       }
     };
-    int tile = 0;
+    int tile0 = 0;
     for (int n_item = 0;; ++n_item) {
       const int slot = n_item % kStepItems, qb = n_item % C::kQBufs;
       // one warp waits and says so to the others: all of them stop together
@@ -649,10 +645,9 @@ __global__ void __launch_bounds__(step_threads<TC>(), 1)
         const int n = threadIdx.x;
         const int rr = it.qt * N + min(n, it.n_rows - 1), tok = a.by_g.div(rr);
         const int p = it.past + tok;
-        sm.pos[n] = p;
         sm.low[n] = first_seen(p, a.window);
         sm.out[n] = ((it.row0 + tok) * a.Hq + it.h * a.G + rr - tok * a.G) * (long long)D;
-        sm.m[n] = 0.0f;
+        sm.m[0][n] = sm.m[1][n] = 0.0f;
         sm.bad[n] = 0;
       }
       named_sync(1, 32 * kStepSoftmax);
@@ -661,34 +656,49 @@ __global__ void __launch_bounds__(step_threads<TC>(), 1)
       const int pos_min = it.past + a.by_g.div(it.qt * N);
       const int pos_max = it.past + a.by_g.div(it.qt * N + it.n_rows - 1);
       const int low_max = first_seen(pos_max, a.window);
-      // e4m3: P carries V's scale, so its sums are not the weights': this
-      // thread's part of those
       float l[kQ8 ? R : 1];
 #pragma unroll
       for (int i = 0; i < (kQ8 ? R : 1); ++i) l[i] = 0.0f;
 
-      for (int j = 0; j < nt; ++j, ++tile) {
-        const int buf = tile & 1;
+      for (int j = (tile0 ^ stream) & 1; j < nt; j += 2) {
+        const int tile = tile0 + j, buf = stream;  // tile & 1
+        const uint32_t phase = (uint32_t)(tile >> 1) & 1u;
         const int k0 = (it.t0 + j) * kStepKeys;
         const int at = k0 + key;
         const bool masked = k0 + kStepKeys > pos_min + 1 || k0 < low_max;
-        const bool first = j == 0 || k0 <= low_max;  // the first keys of some row
+        // rows that see this thread's key: row n of the tile is token (qt N + n) / G
+        int n_lo = 0, n_hi = N;
+        if (masked) {
+          n_lo = max(at - it.past, 0) * a.G - it.qt * N;
+          if (a.window > 0) {
+            const long long e = (long long)at - it.past + a.window;
+            n_hi = (int)max(min(e, (long long)it.n), 0ll) * a.G - it.qt * N;
+            if (e >= it.n) n_hi = N;
+          }
+          // behind the sequence nobody sees, rows that pad included: a score or
+          // scale from there must not even count in the vote
+          if (at >= it.past + it.n) n_lo = N;
+          n_lo -= n0;
+          n_hi -= n0;
+        }
+        // the first keys of some row in this stream's tiles
+        const bool first = j < 2 || k0 - kStepKeys <= low_max;
         float kf = a.scale2, vs = 1.0f, vs2 = 0.0f;
         if constexpr (kQ8) {
           const int sc = tile % kStepScales;
           wait(&sm.scale_full[sc], (uint32_t)(tile / kStepScales) & 1u);
           kf *= sm.scale[sc][0][key];
           vs = sm.scale[sc][1][key];
-          consumed(kf + vs);
           vs2 = fmaxf(__log2f(vs), -60.0f);  // P carries the scale: its size counts
+          consumed(kf + vs2);
           __syncwarp();
           if (lane == 0) mbar_arrive(&sm.scale_empty[sc]);
         }
-        wait(&sm.s_full[buf], (uint32_t)(tile >> 1) & 1u);
+        wait(&sm.s_full[buf], phase);
         tc_fence_after();
         const uint32_t s_col = lane_base + buf * N + n0;
 
-        // scores of kCols rows from row c over the reference, in units of log 2
+        // scores of some rows from row n0 + c over the reference, in units of log 2
         auto load = [&](auto& x, int c, bool over) {
           constexpr int kX = sizeof(x) / 4;
           uint32_t raw[kX];
@@ -697,7 +707,7 @@ __global__ void __launch_bounds__(step_threads<TC>(), 1)
           for (int i = 0; i < kX; i += 4) {
             const int n = n0 + c + i;
             float4 m4 = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-            if (over) m4 = *reinterpret_cast<const float4*>(&sm.m[n]);
+            if (over) m4 = *reinterpret_cast<const float4*>(&sm.m[stream][n]);
             float4 f4 = make_float4(kf, kf, kf, kf);
             if constexpr (kQ8) {
               const float4 q4 = *reinterpret_cast<const float4*>(&sm.qs[qb][n]);
@@ -707,20 +717,68 @@ __global__ void __launch_bounds__(step_threads<TC>(), 1)
             x[i + 1] = fmaf(__uint_as_float(raw[i + 1]), f4.y, -m4.y);
             x[i + 2] = fmaf(__uint_as_float(raw[i + 2]), f4.z, -m4.z);
             x[i + 3] = fmaf(__uint_as_float(raw[i + 3]), f4.w, -m4.w);
-            if (masked) {
-              const int4 p4 = *reinterpret_cast<const int4*>(&sm.pos[n]);
-              const int4 l4 = *reinterpret_cast<const int4*>(&sm.low[n]);
-              if (at > p4.x || at < l4.x) x[i] = -CUDART_INF_F;
-              if (at > p4.y || at < l4.y) x[i + 1] = -CUDART_INF_F;
-              if (at > p4.z || at < l4.z) x[i + 2] = -CUDART_INF_F;
-              if (at > p4.w || at < l4.w) x[i + 3] = -CUDART_INF_F;
-            }
+          }
+          if (masked) {
+#pragma unroll
+            for (int i = 0; i < kX; ++i)
+              if (c + i < n_lo || c + i >= n_hi) x[i] = -CUDART_INF_F;
           }
         };
         float x[kCols];
-        bool hot = kHalfP && first;
-        {
+        bool raise = kHalfP && first, p_free = tile < 2;
+        while (true) {
+          if (raise) {
+            // move the references to the tile's maxima (loops kept short: this
+            // is rare, and its code should not crowd out the rest)
+#pragma unroll 1
+            for (int c = 0; c < R; c += 8) {
+              float y[8];
+              load(y, c, false);
+#pragma unroll
+              for (int i = 0; i < 8; ++i) {
+                const float w = warp_max_redux(y[i] + vs2);
+                if (lane == 0) sm.part[stream][quarter][n0 + c + i] = w;
+              }
+            }
+            named_sync(bar_wg, 128);
+            if (key < R) {
+              const int n = n0 + key;
+              const float old = sm.m[stream][n];
+              const float top = fmaxf(fmaxf(sm.part[stream][0][n], sm.part[stream][1][n]),
+                                      fmaxf(sm.part[stream][2][n], sm.part[stream][3][n]));
+              // whether an earlier tile of this stream has keys of the row
+              const bool seen = j > 1 && k0 - kStepKeys > sm.low[n];
+              const float now = seen ? fmaxf(old, top) : top == -CUDART_INF_F ? old : top;
+              sm.f[stream][n] = seen && now != old ? ex2(old - now) : 1.0f;
+              sm.m[stream][n] = now;
+            }
+            named_sync(bar_wg, 128);
+            if constexpr (kQ8) {
+#pragma unroll
+              for (int i = 0; i < R; ++i) l[i] *= sm.f[stream][n0 + i];
+            }
+            if (j > 1) {
+              // O^T and L hold the tiles up to two before
+              wait(&sm.p_empty[buf], phase ^ 1u);
+              p_free = true;
+              tc_fence_after();
+#pragma unroll 1
+              for (int c = 0; c < (kQ8 ? R : 2 * R); c += 8) {  // O^T, then L
+                const int n = n0 + (c < R ? c : c - R);
+                const uint32_t col = lane_base + (c < R ? kColO : kColL) + stream * N + n;
+                uint32_t o[8];
+                tmem_ld<8>(col, o);
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                  o[i] = __float_as_uint(__uint_as_float(o[i]) * sm.f[stream][n + i]);
+                tmem_st<8>(col, o);
+              }
+              tmem_st_wait();
+            }
+          }
+          // weights, as if no score were outside the range
           float top = -CUDART_INF_F, bottom = CUDART_INF_F;
+          unsigned char* prow = sm.p[buf];
 #pragma unroll
           for (int c = 0; c < R; c += kCols) {
             load(x, c, true);
@@ -731,82 +789,48 @@ __global__ void __launch_bounds__(step_threads<TC>(), 1)
               for (int i = 0; i < kCols; ++i)
                 bottom = fminf(bottom, x[i] == -CUDART_INF_F ? CUDART_INF_F : x[i]);
             }
-          }
-          hot |= top + vs2 > kHot || bottom < -kHot;
-        }
-        if (vote_any(bar_wg, 128, hot)) {
-          // move the references of this warpgroup's rows to their maxima (loops
-          // kept short: this is rare, and its code should not crowd out the rest)
-#pragma unroll 1
-          for (int c = 0; c < R; c += 8) {
-            float y[8];
-            load(y, c, false);
+            uint32_t w[kCols / 2];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              const float w = warp_max_redux(y[i] + vs2);
-              if (lane == 0) sm.part[quarter][n0 + c + i] = w;
-            }
-          }
-          named_sync(bar_wg, 128);
-          if (key < R) {
-            const int n = n0 + key;
-            const float old = sm.m[n];
-            const float top = fmaxf(fmaxf(sm.part[0][n], sm.part[1][n]),
-                                    fmaxf(sm.part[2][n], sm.part[3][n]));
-            const bool seen = j > 0 && k0 > sm.low[n];  // has keys before this tile
-            const float now = seen ? fmaxf(old, top) : top == -CUDART_INF_F ? old : top;
-            sm.f[n] = seen && now != old ? ex2(old - now) : 1.0f;
-            sm.m[n] = now;
-          }
-          named_sync(bar_wg, 128);
-          if constexpr (kQ8) {
-#pragma unroll
-            for (int i = 0; i < R; ++i) l[i] *= sm.f[n0 + i];
-          }
-          if (j > 0) {
-            wait(&sm.p_empty[buf ^ 1], (uint32_t)((tile - 1) >> 1) & 1u);  // O^T, L of tile j - 1
-            tc_fence_after();
-#pragma unroll 1
-            for (int c = 0; c < (kQ8 ? R : 2 * R); c += 8) {  // O^T, then L
-              const int n = n0 + (c < R ? c : c - R);
-              const uint32_t col = lane_base + (c < R ? kColO : kColL) + n;
-              uint32_t o[8];
-              tmem_ld<8>(col, o);
-#pragma unroll
-              for (int i = 0; i < 8; ++i)
-                o[i] = __float_as_uint(__uint_as_float(o[i]) * sm.f[n + i]);
-              tmem_st<8>(col, o);
-            }
-            tmem_st_wait();
-          }
-          if (kLoads == 1) load(x, 0, true);
-        }
-        // weights; the buffer was last read by the MMAs of tile - 2
-        if (tile >= 2) wait(&sm.p_empty[buf], (uint32_t)((tile >> 1) - 1) & 1u);
-        unsigned char* prow = sm.p[buf];
-#pragma unroll
-        for (int c = 0; c < R; c += kCols) {
-          if (kLoads > 1) load(x, c, true);
-#pragma unroll
-          for (int i = 0; i < kCols; i += 8) {
-            uint32_t w[4];
-#pragma unroll
-            for (int y = 0; y < 8; y += 2) {
-              float p0 = ex2(x[i + y]), p1 = ex2(x[i + y + 1]);
-              if constexpr (kQ8) {
-                l[c + i + y] += p0;
-                l[c + i + y + 1] += p1;
+            for (int i = 0; i < kCols; i += 2) {
+              float p0 = ex2(x[i]), p1 = ex2(x[i + 1]);
+              if constexpr (kKeep) {
+                const float q0 = p0, q1 = p1;
+                p0 = x[i] == -CUDART_INF_F ? 0.0f : p0 * vs;
+                p1 = x[i + 1] == -CUDART_INF_F ? 0.0f : p1 * vs;
+                x[i] = q0;
+                x[i + 1] = q1;
+              } else if constexpr (kQ8) {
                 // a masked position's scale may be anything
-                p0 = x[i + y] == -CUDART_INF_F ? 0.0f : p0 * vs;
-                p1 = x[i + y + 1] == -CUDART_INF_F ? 0.0f : p1 * vs;
+                p0 = x[i] == -CUDART_INF_F ? 0.0f : p0 * vs;
+                p1 = x[i + 1] == -CUDART_INF_F ? 0.0f : p1 * vs;
               }
-              w[y / 2] = Pair<TP>::put(p0, p1);
+              w[i / 2] = Pair<TP>::put(p0, p1);
             }
-            *reinterpret_cast<uint4*>(prow + mn_offset<kW>(n0 + c + i, key, kStepKeys)) =
-                make_uint4(w[0], w[1], w[2], w[3]);
+            if (!p_free) {  // the buffer was last read by the MMAs two tiles before
+              wait(&sm.p_empty[buf], phase ^ 1u);
+              p_free = true;
+            }
+#pragma unroll
+            for (int i = 0; i < kCols; i += 8)
+              *reinterpret_cast<uint4*>(prow + mn_offset<kW>(n0 + c + i, key, kStepKeys)) =
+                  make_uint4(w[i / 2], w[i / 2 + 1], w[i / 2 + 2], w[i / 2 + 3]);
+          }
+          if (raise) break;
+          raise = vote_any(bar_wg, 128, top + vs2 > kHot || bottom < -kHot);
+          if (!raise) break;
+        }
+        if constexpr (kQ8) {
+#pragma unroll
+          for (int c = 0; c < R; c += kCols) {
+            if constexpr (!kKeep) {
+              load(x, c, true);
+#pragma unroll
+              for (int i = 0; i < kCols; ++i) x[i] = ex2(x[i]);
+            }
+#pragma unroll
+            for (int i = 0; i < kCols; ++i) l[c + i] += x[i];
           }
         }
-        (void)vs;
         fence_proxy_async_smem();
         tc_fence_before();
         mbar_arrive(&sm.p_full[buf]);
@@ -815,63 +839,111 @@ __global__ void __launch_bounds__(step_threads<TC>(), 1)
         __syncwarp();
         if (lane == 0) mbar_arrive(&sm.q_empty[qb]);  // qs is read
       }
+      tile0 += nt;
 
-      // ---- the item's results: O^T and L of all its keys ----
-      wait(&sm.p_empty[(tile - 1) & 1], (uint32_t)((tile - 1) >> 1) & 1u);
+      // ---- the item's results: both streams' O^T and L, 8 rows a warpgroup ----
+      // (own tiles first: a later wait of the same barrier then means its phase)
+      {
+        const int last = tile0 - 1, prev = tile0 - 2;
+        const int mine = (last & 1) == stream ? last : prev;
+        const int other = (last & 1) == stream ? prev : last;
+        if (mine >= tile0 - nt) wait(&sm.p_empty[mine & 1], (uint32_t)(mine >> 1) & 1u);
+        if (other >= tile0 - nt) wait(&sm.p_empty[other & 1], (uint32_t)(other >> 1) & 1u);
+      }
       tc_fence_after();
       const bool whole = it.part == 0;
       const size_t slot_row = (size_t)(2 * blockIdx.x + (it.part == 2)) * N;
       bool bad = false;
       if constexpr (kQ8) {
-        // the 128 threads' sums, through the P buffers (their MMAs are done)
-        float* ls = reinterpret_cast<float*>(sm.p) + n0 * kStepKeys;
+        // the threads' sums, half of a thread's rows at a time through the P
+        // buffers (their MMAs are done)
+        constexpr int H = R / 2;
+        float* ls = reinterpret_cast<float*>(sm.p) + wg * H * kStepKeys;
 #pragma unroll
-        for (int i = 0; i < R; ++i) ls[i * kStepKeys + key] = l[i];
-        named_sync(bar_wg, 128);
-        constexpr int kPer = 128 / R;  // threads that sum a row
-        const int r = key / kPer;
-        float s = 0.0f;
-#pragma unroll 8
-        for (int i = key % kPer; i < kStepKeys; i += kPer) s += ls[r * kStepKeys + i];
+        for (int hf = 0; hf < 2; ++hf) {
+          named_sync(1, 32 * kStepSoftmax);
 #pragma unroll
-        for (int w = kPer / 2; w > 0; w >>= 1) s += __shfl_xor_sync(0xffffffffu, s, w);
-        if (key % kPer == 0) sm.f[n0 + r] = s;
-        named_sync(bar_wg, 128);
+          for (int i = 0; i < H; ++i) ls[i * kStepKeys + key] = l[hf * H + i];
+          named_sync(bar_wg, 128);
+          constexpr int kPer = 128 / H < 32 ? 128 / H : 32;  // threads that sum a row
+          const int r = key / kPer;
+          float s = 0.0f;
+          if (r < H) {
+#pragma unroll 4
+            for (int i = key % kPer; i < kStepKeys; i += kPer) s += ls[r * kStepKeys + i];
+          }
+#pragma unroll
+          for (int w = kPer / 2; w > 0; w >>= 1) s += __shfl_xor_sync(0xffffffffu, s, w);
+          if (key % kPer == 0 && r < H) sm.f[stream][n0 + hf * H + r] = s;
+        }
       }
+      named_sync(1, 32 * kStepSoftmax);  // both streams' m (and sums)
       if (key < D) {  // uniform over a warp
         // e4m3: V was widened with the elements of four in the order 0 2 1 3
         const int d = kQ8 ? (key & ~3) | (key & 1) << 1 | (key >> 1 & 1) : key;
-        const int last = min(n0 + R, it.n_rows);
+        const int none = nt > 1 ? 2 : tile0 & 1;  // a stream without tiles
 #pragma unroll 1
-        for (int n = n0; n < last; n += 8) {
-          uint32_t o[8], L8[8];
-          tmem_ld8_issue(lane_base + kColO + n, o);
-          if constexpr (!kQ8) tmem_ld8_issue(lane_base + kColL + n, L8);
-          tmem_ld8_wait(o);
-          if constexpr (!kQ8) tmem_ld8_wait(L8);
-          float L[8];
+        for (int n = 8 * wg; n < it.n_rows; n += 32) {
+          uint32_t o[2][8], L8[2][8];
 #pragma unroll
-          for (int i = 0; i < 8; ++i) L[i] = kQ8 ? sm.f[n + i] : __uint_as_float(L8[i]);
+          for (int w = 0; w < 2; ++w) {
+            tmem_ld8_issue(lane_base + kColO + w * N + n, o[w]);
+            if constexpr (!kQ8) tmem_ld8_issue(lane_base + kColL + w * N + n, L8[w]);
+          }
+          tmem_ld8_wait(o[0]);
+          tmem_ld8_wait(o[1]);
+          if constexpr (!kQ8) {
+            tmem_ld8_wait(L8[0]);
+            tmem_ld8_wait(L8[1]);
+          }
+          // (no branches from here to the stores: eight rows side by side)
+          float O[8], Ls[8], M[8];
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            float v[2], L[2], m[2];
+#pragma unroll
+            for (int w = 0; w < 2; ++w) {
+              v[w] = w == none ? 0.0f : __uint_as_float(o[w][i]);
+              L[w] = w == none ? 0.0f : kQ8 ? sm.f[w][n + i] : __uint_as_float(L8[w][i]);
+              // without a visible key there is no reference
+              m[w] = L[w] == 0.0f ? -CUDART_INF_F : sm.m[w][n + i];
+            }
+            M[i] = fmaxf(m[0], m[1]);
+            const float Mu = M[i] == -CUDART_INF_F ? 0.0f : M[i];
+            const float f0 = ex2(m[0] - Mu), f1 = ex2(m[1] - Mu);
+            O[i] = v[0] * f0 + v[1] * f1;
+            Ls[i] = L[0] * f0 + L[1] * f1;
+          }
+          const int rows = it.n_rows - n;
           if (whole) {
+            T* dst = static_cast<T*>(a.out) + d;
+            float worst = 0.0f;
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-              const float r = __uint_as_float(o[i]) * __frcp_rn(L[i]);
-              if (n + i < last) {
-                static_cast<T*>(a.out)[sm.out[n + i] + d] = to_elem<T>(r);
-                if (!isfinite(r)) sm.bad[n + i] = bad = true;
-              }
+              float r;
+              asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(Ls[i]));
+              O[i] *= r;
+              // not a number if any of the rows' results is not finite
+              worst = i < rows ? fmaf(O[i], 0.0f, worst) : worst;
+            }
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+              if (i < rows) dst[sm.out[n + i]] = to_elem<T>(O[i]);
+            if (worst != 0.0f) {
+#pragma unroll
+              for (int i = 0; i < 8; ++i)
+                if (i < rows && !isfinite(O[i])) sm.bad[n + i] = 1;
+              bad = true;
             }
           } else {
             float* dst = parts.o + (slot_row + n) * D + d;
 #pragma unroll
             for (int i = 0; i < 8; ++i)
-              if (n + i < last) dst[i * D] = __uint_as_float(o[i]);
-            if (key == 0) {  // a part without a visible key has no reference
+              if (i < rows) dst[i * D] = O[i];
+            if (key == 0) {
 #pragma unroll
               for (int i = 0; i < 8; ++i)
-                if (n + i < last)
-                  parts.ml[slot_row + n + i] =
-                      make_float2(L[i] == 0.0f ? -CUDART_INF_F : sm.m[n + i], L[i]);
+                if (i < rows) parts.ml[slot_row + n + i] = make_float2(M[i], Ls[i]);
             }
           }
         }
@@ -880,11 +952,13 @@ __global__ void __launch_bounds__(step_threads<TC>(), 1)
       // a result that is not finite may come from a position that its row does
       // not see (0 times infinity): form the row again from those it sees
       if (vote_any(bar_wg, 128, bad)) {
-        for (int n = n0 + quarter; n < n0 + R && n < it.n_rows; n += 4) {
-          if (!sm.bad[n]) continue;
-          const int rr = it.qt * N + n, tok = a.by_g.div(rr);
-          attend_row<T, TC, D>(a, it.b, it.past + tok, it.h * a.G + rr - tok * a.G, it.row0 + tok,
-                               flags);
+        for (int n = 8 * wg; n < it.n_rows; n += 32) {
+          for (int r = n + quarter; r < min(n + 8, it.n_rows); r += 4) {
+            if (!sm.bad[r]) continue;
+            const int rr = it.qt * N + r, tok = a.by_g.div(rr);
+            attend_row<T, TC, D>(a, it.b, it.past + tok, it.h * a.G + rr - tok * a.G,
+                                 it.row0 + tok, flags);
+          }
         }
       }
     }

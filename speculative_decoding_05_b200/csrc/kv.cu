@@ -214,8 +214,9 @@ struct LaunchAttn {
   dspark_status run() {
     if (rows_per_head <= 16) return step<T, TC, Dh, 16>();
     if (rows_per_head <= 32) return step<T, TC, Dh, 32>();
-    if (rows_per_head <= 64) return step<T, TC, Dh, 64>();
-    return step<T, TC, Dh, 128>();
+    if constexpr (sizeof(TC) != 1)
+      if (rows_per_head > 64 && rows_per_head <= 80) return step<T, TC, Dh, 80>();
+    return step<T, TC, Dh, 64>();
   }
 };
 
