@@ -24,14 +24,14 @@
 // at the maximum of the first tile.)
 //
 // e4m3 cache: S^T takes K's codes as they lie, by the 8-bit MMA, and Q as a sum
-// of two e4m3 parts (three for fp16): Q's row, scaled by a power of two to a
-// maximum in [128, 256), is rounded to e4m3 (4 significant bits), the rest
-// rounded again (4 more).  bf16 has 8 and fp16 11 bits, so the sum is exact for
-// elements down to 2^-9 (2^-6) of the row's maximum; below that it is off by at
-// most 2^-17 of the maximum, less than what bf16 itself (2^-8 of the element)
-// rounds off a row of such a spread.  K's scale is applied to the scores.  V's
-// codes are widened to fp16 (exact) by 4 warps, and P is fp16 with V's scale on
-// it: the reference is such that the product stays in fp16's range.
+// of two e4m3 parts (three for fp16): an item's Q, scaled by a power of two to a
+// largest element in [128, 256), is rounded to e4m3 (4 significant bits), the
+// rest rounded again (4 more).  bf16 has 8 and fp16 11 bits, so the sum is exact
+// for elements down to 2^-9 (2^-6) of the largest; below that it is off by at
+// most 2^-17 of the largest, a score then by 2^-17 of what the item's scores can
+// come to, less than the weights' rounding.  K's scale is applied to the scores.
+// V's codes are widened to fp16 (exact) by 4 warps, and P is fp16 with V's scale
+// on it: the reference is such that the product stays in fp16's range.
 //
 // Warps: 16 softmax, one each that loads K (and walks the piece), V and Q, one
 // that issues the MMAs, 4 that widen V (e4m3).  The operands pass in the order
@@ -104,8 +104,8 @@ struct StepSmem {
   alignas(1024) unsigned char in_k[C::kQ8 ? C::kRingK : 1][C::kQ8 ? C::kTileIn : 16];
   alignas(1024) unsigned char in_v[C::kQ8 ? C::kRingV : 1][C::kQ8 ? C::kTileIn : 16];
   float scale[C::kQ8 ? kStepScales : 1][2][kStepKeys];
-  alignas(16) float qs[C::kQBufs][N];         // e4m3: power of two that was taken off a row of Q
-  alignas(16) float m[2][N], f[2][N], part[2][4][N];  // of each stream
+  float qs[2];                      // e4m3: power of two that was taken off Q
+  alignas(16) float neg_m[2][N], f[2][N], part[2][4][N];  // of each stream: -m, ..
   int low[N], bad[N];
   long long out[N];
   uint64_t k_full[C::kRingK], k_empty[C::kRingK];  // 16 bits: of the common ring
@@ -377,74 +377,63 @@ __global__ void __launch_bounds__(step_threads<TC>(), 1)
           alive = false;
           break;
         }
-        constexpr int kChunks = D / 8, kBatch = N * D < 2048 ? 4 : 8;
-        static_assert(!kQ8 || N * kChunks % (32 * kBatch) == 0, "whole batches");
+        constexpr int kChunks = D / 8;
+        auto source = [&](int i) {
+          const int rr = it.qt * N + min(i / kChunks, it.n_rows - 1), tok = a.by_g.div(rr);
+          return static_cast<const T*>(a.q) + (it.row0 + tok) * a.q_stride +
+                 (it.h * a.G + rr - tok * a.G) * D + 8 * (i % kChunks);
+        };
         if constexpr (!kQ8) {
 #pragma unroll 8
+          for (int i = lane; i < N * kChunks; i += 32)
+            cp_async16(sm.q[qb] + sw128_offset(i / kChunks, 8 * (i % kChunks), N), source(i),
+                       i / kChunks < it.n_rows);
+          cp_async_wait_all();
+        } else {
+          // the largest element, then its e4m3 parts
+          float top = 0.0f;
+          bool odd = false;  // fmaxf passes over a NaN
+#pragma unroll 8
+          for (int i = lane; i < N * kChunks; i += 32) {
+            float y[8];
+            unpack8<T>(*reinterpret_cast<const uint4*>(source(i)), y);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+              top = fmaxf(top, fabsf(y[e]));
+              odd |= !isfinite(y[e]);
+            }
+          }
+          top = warp_max(top);
+          odd = __any_sync(0xffffffffu, odd);
+          int e2;
+          frexpf(odd ? 1.0f : top, &e2);
+          const int up = min(8 - e2, 120);  // top 2^up in [128, 256)
+          const float mul = ldexpf(1.0f, up);
+#pragma unroll 4
           for (int i = lane; i < N * kChunks; i += 32) {
             const int r = i / kChunks, c = i % kChunks;
-            const int rr = it.qt * N + min(r, it.n_rows - 1), tok = a.by_g.div(rr);
-            cp_async16(sm.q[qb] + sw128_offset(r, 8 * c, N),
-                       static_cast<const T*>(a.q) + (it.row0 + tok) * a.q_stride +
-                           (it.h * a.G + rr - tok * a.G) * D + 8 * c,
-                       r < it.n_rows);
-          }
-          cp_async_wait_all();
-        }
-#pragma unroll 1
-        for (int i0 = kQ8 ? lane : N * kChunks; i0 < N * kChunks; i0 += 32 * kBatch) {
-          uint4 v[kBatch];
+            uint4 v = *reinterpret_cast<const uint4*>(source(i));
+            if (r >= it.n_rows) v = make_uint4(0, 0, 0, 0);
+            float y[8];
+            unpack8<T>(v, y);
 #pragma unroll
-          for (int x = 0; x < kBatch; ++x) {
-            const int i = i0 + 32 * x, r = i / kChunks, c = i % kChunks;
-            v[x] = make_uint4(0, 0, 0, 0);
-            if (r < it.n_rows) {
-              const int rr = it.qt * N + r, tok = a.by_g.div(rr);
-              v[x] = *reinterpret_cast<const uint4*>(static_cast<const T*>(a.q) +
-                                                     (it.row0 + tok) * a.q_stride +
-                                                     (it.h * a.G + rr - tok * a.G) * D + 8 * c);
+            for (int e = 0; e < 8; ++e) y[e] *= mul;
+#pragma unroll
+            for (int pt = 0; pt < C::kQParts; ++pt) {
+              const uint32_t lo = f32_to_e4m3x4(y[0], y[1], y[2], y[3]);
+              const uint32_t hi = f32_to_e4m3x4(y[4], y[5], y[6], y[7]);
+              *reinterpret_cast<uint2*>(sm.q[qb] + pt * N * D + k8_offset<D>(r, 8 * c)) =
+                  make_uint2(lo, hi);
+              float z[8];
+              e4m3x4_to_f32(lo, z);
+              e4m3x4_to_f32(hi, z + 4);
+#pragma unroll
+              for (int e = 0; e < 8; ++e) y[e] -= z[e];
             }
           }
-#pragma unroll
-          for (int x = 0; x < kBatch; ++x) {
-            const int i = i0 + 32 * x, r = i / kChunks, c = i % kChunks;
-            if constexpr (kQ8) {
-              // e4m3 parts of the row, scaled to a maximum in [128, 256)
-              float y[8], top = 0.0f;
-              unpack8<T>(v[x], y);
-#pragma unroll
-              for (int e = 0; e < 8; ++e) top = fmaxf(top, fabsf(y[e]));
-              bool odd = false;  // fmaxf passes over a NaN
-#pragma unroll
-              for (int e = 0; e < 8; ++e) odd |= !isfinite(y[e]);
-#pragma unroll
-              for (int w = kChunks / 2; w > 0; w >>= 1)
-                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, w));
-              const unsigned odds = __ballot_sync(0xffffffffu, odd);
-              const unsigned mine = (kChunks == 16 ? 0xffffu : 0xffu) << (lane / kChunks * kChunks);
-              int e2;
-              frexpf(top, &e2);
-              const int up = min(8 - e2, 120);  // top 2^up in [128, 256)
-              const float mul = ldexpf(1.0f, up);
-#pragma unroll
-              for (int e = 0; e < 8; ++e) y[e] *= mul;
-#pragma unroll
-              for (int pt = 0; pt < C::kQParts; ++pt) {
-                const uint32_t lo = f32_to_e4m3x4(y[0], y[1], y[2], y[3]);
-                const uint32_t hi = f32_to_e4m3x4(y[4], y[5], y[6], y[7]);
-                *reinterpret_cast<uint2*>(sm.q[qb] + pt * N * D + k8_offset<D>(r, 8 * c)) =
-                    make_uint2(lo, hi);
-                float z[8];
-                e4m3x4_to_f32(lo, z);
-                e4m3x4_to_f32(hi, z + 4);
-#pragma unroll
-                for (int e = 0; e < 8; ++e) y[e] -= z[e];
-              }
-              // a row with a value that is not finite has no such parts: its
-              // results are not finite either way
-              if (c == 0) sm.qs[qb][r] = odds & mine ? CUDART_NAN_F : ldexpf(1.0f, -up);
-            }
-          }
+          // a value that is not finite has no such parts: the item's results
+          // become not finite, and its rows are formed one by one
+          if (lane == 0) sm.qs[qb] = odd ? CUDART_NAN_F : ldexpf(1.0f, -up);
         }
         fence_proxy_async_smem();
         mbar_arrive(&sm.q_full[qb]);
@@ -482,35 +471,35 @@ __global__ void __launch_bounds__(step_threads<TC>(), 1)
     if (!alive) flags |= DSPARK_FLAG_TIMEOUT;
 
   } else if (warp == kStepMma) {
-    // ---- MMA issue ----
+    // ---- MMA issue: one thread ----
     constexpr uint32_t kIdS = kQ8 ? idesc_e4m3(128, N) : idesc_tc<T>(128, N, false, false);
     constexpr uint32_t kIdO = idesc_tc<TP>(128, N, true, true);
     constexpr uint32_t kIdL = idesc_tc<TP>(128, N, false, true);
-    bool alive = true;
-    int op0 = 0, tile0 = 0;
-    for (int n_item = 0;; ++n_item) {
-      const int slot = n_item % kStepItems;
-      if (alive) alive = mbar_wait(&sm.item_full[slot], (uint32_t)(n_item / kStepItems) & 1u);
-      alive = __all_sync(0xffffffffu, alive);
-      if (!alive) break;
-      const int part = sm.item[slot].part, n = sm.item[slot].t1 - sm.item[slot].t0;
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&sm.item_empty[slot]);
-      if (part < 0) break;
-      const int qb = n_item % C::kQBufs;
+    constexpr int kW = C::kW;
+    if (elect_one()) {
+      bool alive = true;
       auto wait = [&](uint64_t* bar, uint32_t parity) {
         if (alive) alive = mbar_wait_spin(bar, parity);
-        alive = __all_sync(0xffffffffu, alive);
       };
-      auto issue_s = [&](int j) {
-        const int use = kQ8 ? tile0 + j : op0 + op_of_k(j), ks = use % C::kRingK;
-        const int buf = (tile0 + j) & 1;
-        wait(&sm.k_full[ks], (uint32_t)(use / C::kRingK) & 1u);
-        tc_fence_after();
-        if (alive && elect_one()) {
+      int op0 = 0, tile0 = 0;
+      for (int n_item = 0;; ++n_item) {
+        const int slot = n_item % kStepItems;
+        wait(&sm.item_full[slot], (uint32_t)(n_item / kStepItems) & 1u);
+        if (!alive) break;
+        const int part = sm.item[slot].part, n = sm.item[slot].t1 - sm.item[slot].t0;
+        consumed(__int_as_float(part + n));
+        mbar_arrive(&sm.item_empty[slot]);
+        if (part < 0) break;
+        const int qb = n_item % C::kQBufs;
+        const uint32_t q_addr = smem_u32(sm.q[qb]);
+        auto issue_s = [&](int j) {
+          const int use = kQ8 ? tile0 + j : op0 + op_of_k(j), ks = use % C::kRingK;
+          const int buf = (tile0 + j) & 1;
+          wait(&sm.k_full[ks], (uint32_t)(use / C::kRingK) & 1u);
+          if (!alive) return;
+          tc_fence_after();
           if constexpr (kQ8) {
-            const uint64_t kd = sdesc_k8<D>(smem_u32(sm.in_k[ks]));
-            const uint64_t qd = sdesc_k8<D>(smem_u32(sm.q[qb]));
+            const uint64_t kd = sdesc_k8<D>(smem_u32(sm.in_k[ks])), qd = sdesc_k8<D>(q_addr);
 #pragma unroll
             for (int pt = 0; pt < C::kQParts; ++pt)
 #pragma unroll
@@ -518,38 +507,34 @@ __global__ void __launch_bounds__(step_threads<TC>(), 1)
                 mma_e4m3_ss(tmem + buf * N, kd + ((k * 32) >> 4), qd + ((pt * N * D + k * 32) >> 4),
                             kIdS, pt > 0 || k > 0);
           } else {
-            const uint64_t kd = sdesc_sw128(smem_u32(sm.op[ks]));
-            const uint64_t qd = sdesc_sw128(smem_u32(sm.q[qb]));
+            const uint64_t kd = sdesc_sw128(smem_u32(sm.op[ks])), qd = sdesc_sw128(q_addr);
 #pragma unroll
             for (int k = 0; k < D / 16; ++k)
               mma_bf16_ss(tmem + buf * N, kd + (((k >> 2) * kStepKeys * 128 + (k & 3) * 32) >> 4),
                           qd + (((k >> 2) * N * 128 + (k & 3) * 32) >> 4), kIdS, k > 0);
           }
-          mma_commit(&sm.k_empty[ks]);
           mma_commit(&sm.s_full[buf]);
+          mma_commit(&sm.k_empty[ks]);
           if (j == n - 1) mma_commit(&sm.q_empty[qb]);
-        }
-        __syncwarp();
-      };
-      wait(&sm.q_full[qb], (uint32_t)(n_item / C::kQBufs) & 1u);
-      issue_s(0);
-      if (n > 1) issue_s(1);
-      for (int j = 0; j < n; ++j) {
-        const int g = tile0 + j, buf = g & 1;
-        wait(&sm.p_full[buf], (uint32_t)(g >> 1) & 1u);
-        // the scores of tile j were read: their buffer takes those of j + 2
-        if (j + 2 < n) issue_s(j + 2);
-        const int use = kQ8 ? g : op0 + op_of_v(j, n), os = use % C::kOps;
-        wait(kQ8 ? &sm.op_full[os] : &sm.k_full[os], (uint32_t)(use / C::kOps) & 1u);
-        if (!kQ8 && j == n - 1) wait(&sm.v_clean[slot], (uint32_t)(n_item / kStepItems) & 1u);
-        tc_fence_after();
-        // V: 64 elements of D in a row, 8 keys 1024 bytes apart, the other 64
-        // behind all keys.  With D = 64 there are no others: lanes 64-127 of
-        // O^T take what lies there and nobody reads them.
-        constexpr int kW = C::kW;
-        const uint64_t vd = sdesc_mn<64>(smem_u32(sm.op[os]), kStepKeys);
-        const uint64_t pd = sdesc_mn<kW>(smem_u32(sm.p[buf]), kStepKeys);
-        if (alive && elect_one()) {
+        };
+        wait(&sm.q_full[qb], (uint32_t)(n_item / C::kQBufs) & 1u);
+        issue_s(0);
+        if (n > 1) issue_s(1);
+        for (int j = 0; j < n; ++j) {
+          const int g = tile0 + j, buf = g & 1;
+          wait(&sm.p_full[buf], (uint32_t)(g >> 1) & 1u);
+          // the scores of tile j were read: their buffer takes those of j + 2
+          if (j + 2 < n) issue_s(j + 2);
+          const int use = kQ8 ? g : op0 + op_of_v(j, n), os = use % C::kOps;
+          wait(kQ8 ? &sm.op_full[os] : &sm.k_full[os], (uint32_t)(use / C::kOps) & 1u);
+          if (!kQ8 && j == n - 1) wait(&sm.v_clean[slot], (uint32_t)(n_item / kStepItems) & 1u);
+          if (!alive) break;
+          tc_fence_after();
+          // V: 64 elements of D in a row, 8 keys 1024 bytes apart, the other 64
+          // behind all keys.  With D = 64 there are no others: lanes 64-127 of
+          // O^T take what lies there and nobody reads them.
+          const uint64_t vd = sdesc_mn<64>(smem_u32(sm.op[os]), kStepKeys);
+          const uint64_t pd = sdesc_mn<kW>(smem_u32(sm.p[buf]), kStepKeys);
 #pragma unroll
           for (int k = 0; k < kStepKeys / 16; ++k)
             mma_bf16_ss(tmem + kColO + buf * N, vd + ((k * 2048) >> 4),
@@ -563,14 +548,12 @@ __global__ void __launch_bounds__(step_threads<TC>(), 1)
           }
           mma_commit(&sm.p_empty[buf]);
         }
-        __syncwarp();
+        op0 += 2 * n;
+        tile0 += n;
       }
-      op0 += 2 * n;
-      tile0 += n;
+      if (!alive) flags |= DSPARK_FLAG_TIMEOUT;
+      drain_mma(&sm.drain);
     }
-    if (!alive) flags |= DSPARK_FLAG_TIMEOUT;
-    // every commit above was the elected lane's: so is the last one
-    if (elect_one()) drain_mma(&sm.drain);
     __syncwarp();
 
   } else if (warp >= kStepWiden) {
@@ -583,6 +566,7 @@ __global__ void __launch_bounds__(step_threads<TC>(), 1)
         const int slot = n_item % kStepItems;
         if (alive) alive = mbar_wait(&sm.item_full[slot], (uint32_t)(n_item / kStepItems) & 1u);
         const int part = sm.item[slot].part, n = sm.item[slot].t1 - sm.item[slot].t0;
+        const int keys = sm.item[slot].past + sm.item[slot].n - sm.item[slot].t0 * kStepKeys;
         // all four warps go on or all stop
         if (vote_any(6, 128, !alive)) {
           alive = false;
@@ -596,7 +580,7 @@ __global__ void __launch_bounds__(step_threads<TC>(), 1)
           if (alive && use >= C::kOps)
             alive = mbar_wait(&sm.op_empty[os], (uint32_t)(use / C::kOps - 1) & 1u);
           if (!alive) break;
-          widen_tile<D>(sm.in_v[vs], sm.op[os], tid);
+          widen_tile<D>(sm.in_v[vs], sm.op[os], keys - j * kStepKeys, tid);
           fence_proxy_async_smem();
           __syncwarp();
           if (lane == 0) {
@@ -647,7 +631,7 @@ __global__ void __launch_bounds__(step_threads<TC>(), 1)
         const int p = it.past + tok;
         sm.low[n] = first_seen(p, a.window);
         sm.out[n] = ((it.row0 + tok) * a.Hq + it.h * a.G + rr - tok * a.G) * (long long)D;
-        sm.m[0][n] = sm.m[1][n] = 0.0f;
+        sm.neg_m[0][n] = sm.neg_m[1][n] = 0.0f;
         sm.bad[n] = 0;
       }
       named_sync(1, 32 * kStepSoftmax);
@@ -691,11 +675,15 @@ __global__ void __launch_bounds__(step_threads<TC>(), 1)
           vs = sm.scale[sc][1][key];
           vs2 = fmaxf(__log2f(vs), -60.0f);  // P carries the scale: its size counts
           consumed(kf + vs2);
+          // a scale behind the sequence may be anything
+          if (at >= it.past + it.n) vs = vs2 = 0.0f;
           __syncwarp();
           if (lane == 0) mbar_arrive(&sm.scale_empty[sc]);
         }
         wait(&sm.s_full[buf], phase);
         tc_fence_after();
+        if constexpr (kQ8) kf *= sm.qs[qb];
+        const uint64_t kf2 = pair_of(kf, kf), vsv = pair_of(vs, vs);
         const uint32_t s_col = lane_base + buf * N + n0;
 
         // scores of some rows from row n0 + c over the reference, in units of log 2
@@ -705,18 +693,14 @@ __global__ void __launch_bounds__(step_threads<TC>(), 1)
           tmem_ld<kX>(s_col + c, raw);
 #pragma unroll
           for (int i = 0; i < kX; i += 4) {
-            const int n = n0 + c + i;
             float4 m4 = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-            if (over) m4 = *reinterpret_cast<const float4*>(&sm.m[stream][n]);
-            float4 f4 = make_float4(kf, kf, kf, kf);
-            if constexpr (kQ8) {
-              const float4 q4 = *reinterpret_cast<const float4*>(&sm.qs[qb][n]);
-              f4 = make_float4(kf * q4.x, kf * q4.y, kf * q4.z, kf * q4.w);
-            }
-            x[i] = fmaf(__uint_as_float(raw[i]), f4.x, -m4.x);
-            x[i + 1] = fmaf(__uint_as_float(raw[i + 1]), f4.y, -m4.y);
-            x[i + 2] = fmaf(__uint_as_float(raw[i + 2]), f4.z, -m4.z);
-            x[i + 3] = fmaf(__uint_as_float(raw[i + 3]), f4.w, -m4.w);
+            if (over) m4 = *reinterpret_cast<const float4*>(&sm.neg_m[stream][n0 + c + i]);
+            pair_to(fma2(pair_of(__uint_as_float(raw[i]), __uint_as_float(raw[i + 1])), kf2,
+                         pair_of(m4.x, m4.y)),
+                    x[i], x[i + 1]);
+            pair_to(fma2(pair_of(__uint_as_float(raw[i + 2]), __uint_as_float(raw[i + 3])), kf2,
+                         pair_of(m4.z, m4.w)),
+                    x[i + 2], x[i + 3]);
           }
           if (masked) {
 #pragma unroll
@@ -743,14 +727,14 @@ __global__ void __launch_bounds__(step_threads<TC>(), 1)
             named_sync(bar_wg, 128);
             if (key < R) {
               const int n = n0 + key;
-              const float old = sm.m[stream][n];
+              const float old = -sm.neg_m[stream][n];
               const float top = fmaxf(fmaxf(sm.part[stream][0][n], sm.part[stream][1][n]),
                                       fmaxf(sm.part[stream][2][n], sm.part[stream][3][n]));
               // whether an earlier tile of this stream has keys of the row
               const bool seen = j > 1 && k0 - kStepKeys > sm.low[n];
               const float now = seen ? fmaxf(old, top) : top == -CUDART_INF_F ? old : top;
               sm.f[stream][n] = seen && now != old ? ex2(old - now) : 1.0f;
-              sm.m[stream][n] = now;
+              sm.neg_m[stream][n] = -now;
             }
             named_sync(bar_wg, 128);
             if constexpr (kQ8) {
@@ -783,7 +767,7 @@ __global__ void __launch_bounds__(step_threads<TC>(), 1)
           for (int c = 0; c < R; c += kCols) {
             load(x, c, true);
 #pragma unroll
-            for (int i = 0; i < kCols; ++i) top = fmaxf(top, x[i]);
+            for (int i = 0; i < kCols; i += 2) top = max3(top, x[i], x[i + 1]);
             if (!kHalfP && first) {
 #pragma unroll
               for (int i = 0; i < kCols; ++i)
@@ -794,16 +778,10 @@ __global__ void __launch_bounds__(step_threads<TC>(), 1)
             for (int i = 0; i < kCols; i += 2) {
               float p0 = ex2(x[i]), p1 = ex2(x[i + 1]);
               if constexpr (kKeep) {
-                const float q0 = p0, q1 = p1;
-                p0 = x[i] == -CUDART_INF_F ? 0.0f : p0 * vs;
-                p1 = x[i + 1] == -CUDART_INF_F ? 0.0f : p1 * vs;
-                x[i] = q0;
-                x[i + 1] = q1;
-              } else if constexpr (kQ8) {
-                // a masked position's scale may be anything
-                p0 = x[i] == -CUDART_INF_F ? 0.0f : p0 * vs;
-                p1 = x[i + 1] == -CUDART_INF_F ? 0.0f : p1 * vs;
+                x[i] = p0;
+                x[i + 1] = p1;
               }
+              if constexpr (kQ8) pair_to(mul2(pair_of(p0, p1), vsv), p0, p1);
               w[i / 2] = Pair<TP>::put(p0, p1);
             }
             if (!p_free) {  // the buffer was last read by the MMAs two tiles before
@@ -828,7 +806,9 @@ __global__ void __launch_bounds__(step_threads<TC>(), 1)
               for (int i = 0; i < kCols; ++i) x[i] = ex2(x[i]);
             }
 #pragma unroll
-            for (int i = 0; i < kCols; ++i) l[c + i] += x[i];
+            for (int i = 0; i < kCols; i += 2)
+              pair_to(add2(pair_of(l[c + i], l[c + i + 1]), pair_of(x[i], x[i + 1])), l[c + i],
+                      l[c + i + 1]);
           }
         }
         fence_proxy_async_smem();
@@ -879,8 +859,7 @@ __global__ void __launch_bounds__(step_threads<TC>(), 1)
       }
       named_sync(1, 32 * kStepSoftmax);  // both streams' m (and sums)
       if (key < D) {  // uniform over a warp
-        // e4m3: V was widened with the elements of four in the order 0 2 1 3
-        const int d = kQ8 ? (key & ~3) | (key & 1) << 1 | (key >> 1 & 1) : key;
+        const int d = key;
         const int none = nt > 1 ? 2 : tile0 & 1;  // a stream without tiles
 #pragma unroll 1
         for (int n = 8 * wg; n < it.n_rows; n += 32) {
@@ -906,7 +885,7 @@ __global__ void __launch_bounds__(step_threads<TC>(), 1)
               v[w] = w == none ? 0.0f : __uint_as_float(o[w][i]);
               L[w] = w == none ? 0.0f : kQ8 ? sm.f[w][n + i] : __uint_as_float(L8[w][i]);
               // without a visible key there is no reference
-              m[w] = L[w] == 0.0f ? -CUDART_INF_F : sm.m[w][n + i];
+              m[w] = L[w] == 0.0f ? -CUDART_INF_F : -sm.neg_m[w][n + i];
             }
             M[i] = fmaxf(m[0], m[1]);
             const float Mu = M[i] == -CUDART_INF_F ? 0.0f : M[i];

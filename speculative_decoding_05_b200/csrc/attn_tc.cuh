@@ -175,35 +175,72 @@ __device__ __forceinline__ void cp_async_wait_all() {
   asm volatile("cp.async.wait_all;" ::: "memory");
 }
 
-// Four e4m3 codes as fp16, the pairs (0, 2) and (1, 3) (exact).  A code in the
-// high byte of a half is s eeee mmm; shifted right by one behind its sign the
-// exponent lands on the low four of fp16's five bits (subnormal codes on its
-// subnormals), and 2^8 makes up for the difference of the biases, 15 - 7.
+// Pairs of fp32 operations in one instruction.
+__device__ __forceinline__ uint64_t pair_of(float a, float b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ void pair_to(uint64_t v, float& a, float& b) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+// The largest of three (a NaN is passed over).
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+
+// Four e4m3 codes as fp16 (exact).
 __device__ __forceinline__ uint2 widen4(uint32_t c) {
-  const uint32_t even = ((c << 7) & 0x3f803f80u) | ((c << 8) & 0x80008000u);
-  const uint32_t odd = ((c >> 1) & 0x3f803f80u) | (c & 0x80008000u);
-  const __half2 f = __floats2half2_rn(256.0f, 256.0f);
-  const __half2 x = __hmul2(*reinterpret_cast<const __half2*>(&even), f);
-  const __half2 y = __hmul2(*reinterpret_cast<const __half2*>(&odd), f);
-  return make_uint2(*reinterpret_cast<const uint32_t*>(&x), *reinterpret_cast<const uint32_t*>(&y));
+  uint2 r;
+  asm("{\n\t.reg .b16 lo, hi;\n\t"
+      "mov.b32 {lo, hi}, %2;\n\t"
+      "cvt.rn.f16x2.e4m3x2 %0, lo;\n\t"
+      "cvt.rn.f16x2.e4m3x2 %1, hi;\n\t}"
+      : "=r"(r.x), "=r"(r.y)
+      : "r"(c));
+  return r;
 }
 
 // An e4m3 tile of 128 rows x D bytes (as TMA wrote it, swizzled over its row) to
 // fp16 in the operands' layout (64-element halves, 128-byte swizzle), by 128
-// threads; elements of four in the order 0 2 1 3.
+// threads; rows from `rows` on become zero: what lies behind a sequence may be
+// anything, and 0 times a NaN is none.  (Loops kept short: the warps of a CTA run different code, and what
+// does not fit the instruction cache of an SM's quarter costs more than it saves.)
 template <int D>
-__device__ __forceinline__ void widen_tile(const unsigned char* raw, unsigned char* op, int tid) {
+__device__ __forceinline__ void widen_tile(const unsigned char* raw, unsigned char* op, int rows,
+                                           int tid) {
   constexpr int kChunks = D / 16, kBatch = 4;
   const int c = tid % kChunks;
   // the halves of D lie on the same banks: their lanes take the two halves of
   // their 16 bytes in opposite order
   const bool swap = c & 4;
-#pragma unroll
+#pragma unroll 1
   for (int i0 = tid; i0 < 128 * kChunks; i0 += 128 * kBatch) {
     uint4 u[kBatch];
 #pragma unroll
     for (int b = 0; b < kBatch; ++b)
-      u[b] = *reinterpret_cast<const uint4*>(raw + k8_offset<D>((i0 + 128 * b) / kChunks, 16 * c));
+    {
+      const int row = (i0 + 128 * b) / kChunks;
+      u[b] = *reinterpret_cast<const uint4*>(raw + k8_offset<D>(row, 16 * c));
+      if (row >= rows) u[b] = make_uint4(0, 0, 0, 0);
+    }
 #pragma unroll
     for (int b = 0; b < kBatch; ++b) {
       const int row = (i0 + 128 * b) / kChunks;

@@ -112,8 +112,9 @@ def attention(p, sm_scale=None, window=0):
 
     e4m3: the weights are fp16 with V's scale on them, the largest such product
     at least 1, so half the smallest step is against max|v| again.  Queries are
-    sums of e4m3 parts, off by at most 2^-17 of the row's largest element each:
-    a score by 2^-17 max|q| sum|k| scale."""
+    sums of e4m3 parts, off by at most 2^-17 of the largest element of the rows
+    formed together (at most the request's for the key head): a score by 2^-17
+    max|q| sum|k| scale."""
     sm_scale = p.D ** -0.5 if sm_scale is None else sm_scale
     u_p = half_step(torch.bfloat16 if p.cache == torch.bfloat16 else torch.float16)
     u_o = half_step(p.act)
@@ -149,7 +150,8 @@ def attention(p, sm_scale=None, window=0):
                 o[rows] = o[rows] + bad
             A = w @ va.abs()
             if p.cache == torch.float8_e4m3fn:
-                part = 2.0 ** -17 * sm_scale * q[:, h].abs().amax(-1, True) * kh.abs().sum(-1)
+                most = q[:, h // G * G:(h // G + 1) * G].abs().amax()
+                part = 2.0 ** -17 * sm_scale * most * kh.abs().sum(-1).expand(n, -1)
                 S8 = part.masked_fill(~seen, 0).amax(-1, True)
             else:
                 S8 = 0.0
