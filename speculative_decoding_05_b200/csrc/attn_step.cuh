@@ -103,7 +103,7 @@ struct StepSmem {
   unsigned char behind[C::kBehind];
   alignas(1024) unsigned char in_k[C::kQ8 ? C::kRingK : 1][C::kQ8 ? C::kTileIn : 16];
   alignas(1024) unsigned char in_v[C::kQ8 ? C::kRingV : 1][C::kQ8 ? C::kTileIn : 16];
-  float scale[C::kQ8 ? kStepScales : 1][2][kStepKeys];
+  alignas(16) float scale[C::kQ8 ? kStepScales : 1][2][kStepKeys];
   float qs[2];                      // e4m3: power of two that was taken off Q
   alignas(16) float neg_m[2][N], f[2][N], part[2][4][N];  // of each stream: -m, ..
   int low[N], bad[N];
@@ -182,7 +182,7 @@ __global__ void __launch_bounds__(step_threads<TC>(), 1)
       mbar_init(&sm.op_empty[i], 1);
     }
     for (int i = 0; i < kStepScales; ++i) {
-      mbar_init(&sm.scale_full[i], 1);
+      mbar_init(&sm.scale_full[i], 32);
       mbar_init(&sm.scale_empty[i], kStepSoftmax / 2);
     }
     for (int i = 0; i < 2; ++i) {
@@ -298,17 +298,24 @@ __global__ void __launch_bounds__(step_threads<TC>(), 1)
         for (int i = 0; i < kStepKeys / 16; ++i) y[i] = __shfl_sync(0xffffffffu, y_mine, i);
         // use of the ring: 16 bits, the operand's place in the common order
         const int use = kQ8 ? tile0 + j : op0 + (is_k ? op_of_k(j) : op_of_v(j, n));
-        const int ring = is_k ? C::kRingK : C::kRingV;
-        const int stage = use % ring;
-        if (!kQ8 && lane == 0) *my_next = use;
-        if (use >= ring) {
+        int stage;
+        bool again;
+        uint32_t parity;  // of the stage's release
+        if constexpr (kQ8) {
+          stage = is_k ? use % C::kRingK : use % C::kRingV;
+          again = use >= (is_k ? C::kRingK : C::kRingV);
+          parity = (uint32_t)((is_k ? use / C::kRingK : use / C::kRingV) - 1) & 1u;
+        } else {
+          stage = use % C::kOps;
+          again = use >= C::kOps;
+          parity = (uint32_t)(use / C::kOps - 1) & 1u;
+          if (lane == 0) *my_next = use;
           // The wait for the stage's release tells phases apart by parity only.
-          // In the common ring its last use may be the other warp's: once that
-          // is filled the use before it has been released, and the parity can
-          // mean one phase only.
-          if (!kQ8 && !next_past(other_next, use - ring)) alive = false;
-          if (alive) alive = mbar_wait(&empty[stage], (uint32_t)(use / ring - 1) & 1u);
+          // Its last use may be the other warp's: once that is filled the use
+          // before it has been released, and the parity can mean one phase only.
+          if (again && !next_past(other_next, use - C::kOps)) alive = false;
         }
+        if (again && alive) alive = mbar_wait(&empty[stage], parity);
         const int sc = (tile0 + j) % kStepScales;
         if (alive && kQ8 && is_k && tile0 + j >= kStepScales)
           alive = mbar_wait(&sm.scale_empty[sc], (uint32_t)((tile0 + j) / kStepScales - 1) & 1u);
@@ -318,7 +325,6 @@ __global__ void __launch_bounds__(step_threads<TC>(), 1)
         }
         if (elect_one()) {
           mbar_arrive_expect_tx(&full[stage], (boxes << box_shift) * D * (int)sizeof(TC));
-          if (kQ8 && is_k) mbar_arrive_expect_tx(&sm.scale_full[sc], (boxes << box_shift) * 8);
           unsigned char* dst = !kQ8 ? sm.op[stage] : is_k ? sm.in_k[stage] : sm.in_v[stage];
           const CUtensorMap* map = is_k ? &mk : &mv;
           constexpr int kWidth = kQ8 && D == 64 ? 64 : 128;
@@ -330,15 +336,18 @@ __global__ void __launch_bounds__(step_threads<TC>(), 1)
               for (int hf = 0; hf < kHalves; ++hf)
                 tma_load_2d(dst + hf * kStepKeys * 128 + (i << box_shift) * kWidth, map,
                             &full[stage], hf * 64, y[i]);
-              if (kQ8 && is_k) {
-                const uint64_t pol = policy_evict_first();
-                bulk_load(&sm.scale[sc][0][i << box_shift], a.k_scale + y[i], box_rows * 4,
-                          &sm.scale_full[sc], pol);
-                bulk_load(&sm.scale[sc][1][i << box_shift], a.v_scale + y[i], box_rows * 4,
-                          &sm.scale_full[sc], pol);
-              }
             }
           }
+        }
+        __syncwarp();
+        if (kQ8 && is_k) {
+          // scales, 4 keys a lane; every lane arrives when its copies are there
+          const int box = min(lane * 4 >> box_shift, boxes - 1);
+          const long long at = __shfl_sync(0xffffffffu, y_mine, box) + (lane * 4 & (box_rows - 1));
+          const bool take = lane * 4 >> box_shift < boxes;
+          cp_async16(&sm.scale[sc][0][lane * 4], a.k_scale + at, take);
+          cp_async16(&sm.scale[sc][1][lane * 4], a.v_scale + at, take);
+          cp_async_arrive(&sm.scale_full[sc]);
         }
         __syncwarp();
         if (lane == 0) {  // for the drain after an abort

@@ -171,6 +171,12 @@ __device__ __forceinline__ void cp_async16(void* dst, const void* src, bool take
                "r"(take ? 16 : 0)
                : "memory");
 }
+// Arrives on `bar` (as one of its expected arrivals) once this thread's copies
+// so far are there.
+__device__ __forceinline__ void cp_async_arrive(uint64_t* bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar))
+               : "memory");
+}
 __device__ __forceinline__ void cp_async_wait_all() {
   asm volatile("cp.async.wait_all;" ::: "memory");
 }
