@@ -33,8 +33,8 @@
 // V's codes are widened to fp16 (exact) by 4 warps, and P is fp16 with V's scale
 // on it: the reference is such that the product stays in fp16's range.
 //
-// Warps: 16 softmax, one each that loads K (and walks the piece), V and Q, one
-// that issues the MMAs, 4 that widen V (e4m3).  The operands pass in the order
+// Warps: 16 softmax, one each that loads K (and walks the piece), V, and Q (and
+// scales), one that issues the MMAs, 4 that widen V (e4m3).  The operands pass in the order
 // K0 K1 K2 V0 K3 V1 ..: scores are formed two tiles ahead, as far as their two
 // buffers reach.
 #pragma once
@@ -124,7 +124,7 @@ struct StepSmem {
   unsigned flags;
   int stop;
   int next_k, next_v;               // operand that the K and the V warp issue next, at least
-  int last_k, last_v, last_tile;    // issued last
+  int last_k, last_v;               // issued last
 };
 
 // Place of tile j's K and V in the operand order K0 K1 K2 V0 K3 V1 .. of an item
@@ -199,7 +199,7 @@ __global__ void __launch_bounds__(step_threads<TC>(), 1)
     }
     mbar_init(&sm.drain, 1);
     sm.flags = 0;
-    sm.last_k = sm.last_v = sm.last_tile = -1;
+    sm.last_k = sm.last_v = -1;
     sm.next_k = sm.next_v = 0;
     fence_barrier_init();
   }
@@ -316,9 +316,6 @@ __global__ void __launch_bounds__(step_threads<TC>(), 1)
           if (again && !next_past(other_next, use - C::kOps)) alive = false;
         }
         if (again && alive) alive = mbar_wait(&empty[stage], parity);
-        const int sc = (tile0 + j) % kStepScales;
-        if (alive && kQ8 && is_k && tile0 + j >= kStepScales)
-          alive = mbar_wait(&sm.scale_empty[sc], (uint32_t)((tile0 + j) / kStepScales - 1) & 1u);
         if (!__all_sync(0xffffffffu, alive)) {
           alive = false;
           break;
@@ -340,19 +337,8 @@ __global__ void __launch_bounds__(step_threads<TC>(), 1)
           }
         }
         __syncwarp();
-        if (kQ8 && is_k) {
-          // scales, 4 keys a lane; every lane arrives when its copies are there
-          const int box = min(lane * 4 >> box_shift, boxes - 1);
-          const long long at = __shfl_sync(0xffffffffu, y_mine, box) + (lane * 4 & (box_rows - 1));
-          const bool take = lane * 4 >> box_shift < boxes;
-          cp_async16(&sm.scale[sc][0][lane * 4], a.k_scale + at, take);
-          cp_async16(&sm.scale[sc][1][lane * 4], a.v_scale + at, take);
-          cp_async_arrive(&sm.scale_full[sc]);
-        }
-        __syncwarp();
         if (lane == 0) {  // for the drain after an abort
           *(is_k ? &sm.last_k : &sm.last_v) = use;
-          if (is_k) sm.last_tile = tile0 + j;
         }
       }
       op0 += 2 * n;
@@ -363,10 +349,10 @@ __global__ void __launch_bounds__(step_threads<TC>(), 1)
     if (lane == 0 && is_k) parts.rec[blockIdx.x] = rec;
 
   } else if (warp == kStepLoadQ) {
-    // ---- Q rows to shared memory (rows behind the last are zero); V cleared
-    //      behind the end of a sequence ----
+    // ---- Q rows to shared memory (rows behind the last are zero); 16 bits: V
+    //      cleared behind the end of a sequence; e4m3: scales ----
     bool alive = true;
-    int op0 = 0, n_before = 0;
+    int op0 = 0, n_before = 0, tile = 0;
     Item before;
     before.part = -1;
     for (int n_item = 0;; ++n_item) {
@@ -447,6 +433,39 @@ __global__ void __launch_bounds__(step_threads<TC>(), 1)
         fence_proxy_async_smem();
         mbar_arrive(&sm.q_full[qb]);
       }
+      if constexpr (kQ8) {
+        // (Q of the next item comes behind the last of these, some tiles before
+        // it is used)
+        const int n = it.part >= 0 ? it.t1 - it.t0 : 0;
+        const int shift = a.rows.page_shift, in_page = (1 << shift) - 1;
+        const int* table = a.rows.page_table + (it.part >= 0 ? (size_t)it.b * a.rows.max_pages : 0);
+        const int last_key = it.past + it.n;
+        // a lane's 4 keys lie in one page; its id is read a tile ahead
+        auto page_of = [&](int j) {
+          const int k = (it.t0 + j) * kStepKeys + 4 * lane;
+          return j < n && k < last_key ? __ldg(table + (k >> shift)) : 0;
+        };
+        int page = page_of(0);
+#pragma unroll 1
+        for (int j = 0; j < n; ++j, ++tile) {
+          const int k = (it.t0 + j) * kStepKeys + 4 * lane;
+          int pid = page;
+          if ((unsigned)pid >= (unsigned)a.rows.n_pages) pid = 0;  // flagged with its tile
+          const long long at = (((long long)pid * a.Hkv + it.h) << shift) + (k & in_page);
+          page = page_of(j + 1);
+          const int sc = tile % kStepScales;
+          if (tile >= kStepScales)
+            alive = mbar_wait(&sm.scale_empty[sc], (uint32_t)(tile / kStepScales - 1) & 1u);
+          if (!__all_sync(0xffffffffu, alive)) {
+            alive = false;
+            break;
+          }
+          cp_async16(&sm.scale[sc][0][lane * 4], a.k_scale + at, k < last_key);
+          cp_async16(&sm.scale[sc][1][lane * 4], a.v_scale + at, k < last_key);
+          cp_async_arrive(&sm.scale_full[sc]);
+        }
+        if (!alive) break;
+      }
       if (!kQ8 && before.part >= 0) {
         // What lies behind the sequence in its last page may be anything, and 0
         // times an infinity is none: clear those rows of the last V tile.  One
@@ -477,6 +496,7 @@ __global__ void __launch_bounds__(step_threads<TC>(), 1)
       before = it;
       n_before = it.t1 - it.t0;
     }
+    if (kQ8) cp_async_wait_all();
     if (!alive) flags |= DSPARK_FLAG_TIMEOUT;
 
   } else if (warp == kStepMma) {
@@ -964,8 +984,6 @@ __global__ void __launch_bounds__(step_threads<TC>(), 1)
       if (kQ8) {
         for (int u = max(sm.last_v - C::kRingV + 1, 0); u <= sm.last_v; ++u)
           mbar_wait(&sm.v_full[u % C::kRingV], (uint32_t)(u / C::kRingV) & 1u);
-        for (int t = max(sm.last_tile - kStepScales + 1, 0); t <= sm.last_tile; ++t)
-          mbar_wait(&sm.scale_full[t % kStepScales], (uint32_t)(t / kStepScales) & 1u);
       }
     }
     __syncthreads();
