@@ -389,22 +389,27 @@ def _kv_type(t, what):
     return code
 
 
+def _kv_refuse(what, t, shape, dtype, device):
+    raise ValueError(f"{what}: want a contiguous {dtype} tensor of shape {tuple(shape)} on {device}, "
+                     f"got {t.dtype} {tuple(t.shape)} with strides {t.stride()} on {t.device}")
+
+
 def _kv_want(what, t, shape, dtype, device):
-    if tuple(t.shape) != shape or t.dtype != dtype or t.device != device or not t.is_contiguous():
-        raise ValueError(f"{what}: want a contiguous {dtype} tensor of shape {shape} on {device}, "
-                         f"got {t.dtype} {tuple(t.shape)} with strides {t.stride()} on {t.device}")
+    if t.shape != shape or t.dtype != dtype or t.device != device or not t.is_contiguous():
+        _kv_refuse(what, t, shape, dtype, device)
 
 
 def _kv_rows(what, t, n_rows, D, device, dtype):
     """A row tensor [n_rows, H, D] whose rows may be apart: (H, row stride)."""
-    if (t.dim() != 3 or t.shape[0] != n_rows or t.shape[2] != D or t.dtype != dtype
-            or t.device != device or (t.shape[1] * D > 0 and n_rows > 0
-                                      and (t.stride(2) != 1 or t.stride(1) != D))):
-        raise ValueError(f"{what}: want {dtype} rows [{n_rows}, heads, {D}] with contiguous heads "
-                         f"on {device}, got {t.dtype} {tuple(t.shape)} with strides {t.stride()} "
-                         f"on {t.device}")
-    H = t.shape[1]
-    return H, (t.stride(0) if n_rows > 1 else H * D)
+    if t.dim() == 3 and t.dtype == dtype and t.device == device:
+        n, H, d = t.shape
+        if n == n_rows and d == D:
+            rs, hs, es = t.stride()
+            if (hs == D and es == 1) or n * H * D == 0:
+                return H, (rs if n_rows > 1 else H * D)
+    raise ValueError(f"{what}: want {dtype} rows [{n_rows}, heads, {D}] with contiguous heads on "
+                     f"{device}, got {t.dtype} {tuple(t.shape)} with strides {t.stride()} on "
+                     f"{t.device}")
 
 
 def _kv_cache(k_cache, v_cache, k_scale, v_scale, row_start, verify_len, cache_len, page_table):
@@ -412,11 +417,11 @@ def _kv_cache(k_cache, v_cache, k_scale, v_scale, row_start, verify_len, cache_l
     Hkv, page_size, D, B, max_pages, device)."""
     if k_cache.dim() != 4:
         raise ValueError(f"k_cache: want [n_pages, Hkv, page_size, D], got {tuple(k_cache.shape)}")
+    dtype, dev, shape = k_cache.dtype, k_cache.device, k_cache.shape
     code = _kv_type(k_cache, "k_cache")
-    dev = k_cache.device
-    shape = tuple(k_cache.shape)
-    _kv_want("k_cache", k_cache, shape, k_cache.dtype, dev)
-    _kv_want("v_cache", v_cache, shape, k_cache.dtype, dev)
+    if not k_cache.is_contiguous():
+        _kv_refuse("k_cache", k_cache, shape, dtype, dev)
+    _kv_want("v_cache", v_cache, shape, dtype, dev)
     if code == DSPARK_KV_E4M3:
         if k_scale is None or v_scale is None:
             raise ValueError("an e4m3 cache needs k_scale and v_scale")
@@ -427,27 +432,41 @@ def _kv_cache(k_cache, v_cache, k_scale, v_scale, row_start, verify_len, cache_l
     if page_table.dim() != 2:
         raise ValueError(f"page_table: want [B, max_pages], got {tuple(page_table.shape)}")
     B, max_pages = page_table.shape
+    per = (B,)
     _kv_want("page_table", page_table, (B, max_pages), torch.int32, dev)
-    _kv_want("row_start", row_start, (B,), torch.int64, dev)
-    _kv_want("verify_len", verify_len, (B,), torch.int32, dev)
-    _kv_want("cache_len", cache_len, (B,), torch.int32, dev)
+    _kv_want("row_start", row_start, per, torch.int64, dev)
+    _kv_want("verify_len", verify_len, per, torch.int32, dev)
+    _kv_want("cache_len", cache_len, per, torch.int32, dev)
     return (code, *shape, B, max_pages, dev)
 
 
-def _kv_call(name, device, workspace, stream, args):
+# The raw handle of a device's current stream, as compiled extensions of torch
+# take it; torch.cuda.current_stream builds an object for it (3 us a call).
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _kv_call(fn, device, workspace, stream, args):
     """Calls the library with the tensors' device current, on `stream` or
     that device's current stream."""
     if workspace.device != device:
-        raise ValueError(f"{name}: the workspace is on {workspace.device}, the tensors on {device}")
-    fn = getattr(load(), name)
+        raise ValueError(f"{fn.__name__}: the workspace is on {workspace.device}, the tensors on "
+                         f"{device}")
     ws, n = workspace.data_ptr(), workspace.numel() * workspace.element_size()
     if device.type != "cuda":  # refused calls come back before any launch
         rc = fn(*args, ws, n, stream.cuda_stream if stream is not None else 0)
     else:
-        with torch.cuda.device(device):
-            s = stream if stream is not None else torch.cuda.current_stream()
-            rc = fn(*args, ws, n, s.cuda_stream)
-    _check(name, rc)
+        i = device.index
+        if stream is not None:
+            s = stream.cuda_stream
+        else:
+            s = _raw_stream(i) if _raw_stream else torch.cuda.current_stream(device).cuda_stream
+        if i == torch.cuda.current_device():
+            rc = fn(*args, ws, n, s)
+        else:
+            with torch.cuda.device(device):
+                rc = fn(*args, ws, n, s)
+    if rc != 0:
+        raise DSparkError(fn.__name__, rc)
 
 
 def dspark_kv_workspace_size() -> int:
@@ -477,12 +496,12 @@ def dspark_kv_append(q, k, v, row_start, verify_len, cache_len, page_table, k_ca
     if inv_freq is not None:
         rot = 2 * inv_freq.numel()
         _kv_want("inv_freq", inv_freq, (rot // 2,), torch.float64, dev)
-    _kv_call("dspark_kv_append", dev, workspace, stream,
-             (_at(q), _at(k), _at(v), qs, ks, vs, act, n_rows, B, Hq, Hkv, D, _at(row_start),
-              _at(verify_len), _at(cache_len), _at(page_table), max_pages, _at(k_cache),
-              _at(v_cache), _at(k_scale), _at(v_scale), code, n_pages, ps, _at(q_norm),
+    _kv_call(load().dspark_kv_append, dev, workspace, stream,
+             (q.data_ptr(), k.data_ptr(), v.data_ptr(), qs, ks, vs, act, n_rows, B, Hq, Hkv, D, row_start.data_ptr(),
+              verify_len.data_ptr(), cache_len.data_ptr(), page_table.data_ptr(), max_pages, k_cache.data_ptr(),
+              v_cache.data_ptr(), _at(k_scale), _at(v_scale), code, n_pages, ps, _at(q_norm),
               _at(k_norm), eps, _at(inv_freq), rot, int(bool(interleaved)), rope_scale,
-              _at(q_out)))
+              q_out.data_ptr()))
 
 
 def dspark_kv_read(k_cache, v_cache, row_start, verify_len, cache_len, page_table, k_out, v_out,
@@ -494,10 +513,10 @@ def dspark_kv_read(k_cache, v_cache, row_start, verify_len, cache_len, page_tabl
     n_rows = k_out.shape[0]
     _kv_want("k_out", k_out, (n_rows, Hkv, D), k_out.dtype, dev)
     _kv_want("v_out", v_out, (n_rows, Hkv, D), k_out.dtype, dev)
-    _kv_call("dspark_kv_read", dev, workspace, stream,
-             (_at(k_cache), _at(v_cache), _at(k_scale), _at(v_scale), code, n_pages, ps,
-              _at(row_start), _at(verify_len), _at(cache_len), _at(page_table), max_pages, n_rows,
-              B, Hkv, D, _at(k_out), _at(v_out), _kv_type(k_out, "k_out")))
+    _kv_call(load().dspark_kv_read, dev, workspace, stream,
+             (k_cache.data_ptr(), v_cache.data_ptr(), _at(k_scale), _at(v_scale), code, n_pages, ps,
+              row_start.data_ptr(), verify_len.data_ptr(), cache_len.data_ptr(), page_table.data_ptr(), max_pages, n_rows,
+              B, Hkv, D, k_out.data_ptr(), v_out.data_ptr(), _kv_type(k_out, "k_out")))
 
 
 def dspark_attn_workspace_size(B, Hq, Hkv, D, max_len) -> int:
@@ -515,8 +534,8 @@ def dspark_attn_verify(q, k_cache, v_cache, row_start, verify_len, cache_len, pa
     act = _kv_type(q, "q")
     Hq, qs = _kv_rows("q", q, n_rows, D, dev, q.dtype)
     _kv_want("out", out, (n_rows, Hq, D), q.dtype, dev)
-    _kv_call("dspark_attn_verify", dev, workspace, stream,
-             (_at(q), qs, act, n_rows, B, Hq, Hkv, D, max_len, _at(row_start), _at(verify_len),
-              _at(cache_len), _at(page_table), max_pages, _at(k_cache), _at(v_cache),
+    _kv_call(load().dspark_attn_verify, dev, workspace, stream,
+             (q.data_ptr(), qs, act, n_rows, B, Hq, Hkv, D, max_len, row_start.data_ptr(), verify_len.data_ptr(),
+              cache_len.data_ptr(), page_table.data_ptr(), max_pages, k_cache.data_ptr(), v_cache.data_ptr(),
               _at(k_scale), _at(v_scale), code, n_pages, ps,
-              D ** -0.5 if sm_scale is None else sm_scale, window, _at(out)))
+              D ** -0.5 if sm_scale is None else sm_scale, window, out.data_ptr()))
