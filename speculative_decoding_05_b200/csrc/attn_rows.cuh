@@ -7,25 +7,6 @@
 
 namespace dspark {
 
-// Division of 0 <= x < 2^31 by a divisor known on the host: with l = ceil(log2 d)
-// and m = floor(2^(31 + l) / d) + 1, x m / 2^(31 + l) exceeds x / d by less than
-// x / 2^(31 + l) <= 1 / d, so its whole part is the quotient.
-struct Divisor {
-  unsigned m;
-  int shift;
-  __device__ __forceinline__ int div(int x) const {
-    return (int)(((unsigned long long)(unsigned)x * m) >> shift);
-  }
-};
-inline Divisor make_divisor(int d) {
-  int l = 0;
-  while ((1 << l) < d) ++l;
-  Divisor r;
-  r.m = (unsigned)((1ull << (31 + l)) / (unsigned)d + 1);
-  r.shift = 31 + l;
-  return r;
-}
-
 struct AttnArgs {
   KvRows rows;
   const void* q;

@@ -126,8 +126,10 @@ dspark_status dispatch(const Common& c, F&& f) {
   return q8 ? f.template run<T, e4m3, 64>() : f.template run<T, T, 64>();
 }
 
-int row_grid(long long n_rows) {
-  const long long most = 8ll * kv_sms();
+// Blocks of the row kernels: at most `per_sm` on an SM, all at once (a block
+// takes runs of tokens until none are left).
+int row_grid(long long n_rows, int per_sm) {
+  const long long most = (long long)per_sm * kv_sms();
   const long long g = n_rows < most ? n_rows : most;
   return (int)(g < kMaxStatusCtas ? g : kMaxStatusCtas);
 }
@@ -291,7 +293,7 @@ dspark_status dspark_kv_append(
   if ((st = check_pointers(c)) != DSPARK_OK) return st;
   if (!q || !k || !v || !q_out) return DSPARK_ERR_INVALID_ARG;
   if (!aligned(q, 16) || !aligned(k, 16) || !aligned(v, 16) || !aligned(q_out, 16) ||
-      !aligned(q_norm, 4) || !aligned(k_norm, 4) || !aligned(inv_freq, 8))
+      !aligned(q_norm, 16) || !aligned(k_norm, 16) || !aligned(inv_freq, 8))
     return DSPARK_ERR_INVALID_ARG;
   LaunchAppend l;
   AppendArgs& a = l.a;
@@ -306,7 +308,9 @@ dspark_status dspark_kv_append(
   a.status = static_cast<unsigned*>(workspace);
   a.eps = eps; a.rope_scale = rope_scale;
   a.Hq = Hq; a.Hkv = Hkv; a.rot = rot_dim; a.interleaved = interleaved != 0;
-  l.grid = row_grid(n_rows);
+  a.by_hq = make_divisor(Hq);
+  a.by_hkv = make_divisor(Hkv);
+  l.grid = row_grid(n_rows, 4);
   l.s = s;
   return dispatch(c, l);
 }
@@ -336,7 +340,7 @@ dspark_status dspark_kv_read(
   a.k_out = k_out; a.v_out = v_out;
   a.status = static_cast<unsigned*>(workspace);
   a.Hkv = Hkv;
-  l.grid = row_grid(n_rows);
+  l.grid = row_grid(n_rows, 6);
   l.s = s;
   return dispatch(c, l);
 }

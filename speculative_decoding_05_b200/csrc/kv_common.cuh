@@ -121,6 +121,49 @@ __device__ __forceinline__ int find_request(const int* s_first, int B, int i) {
   return lo;
 }
 
+// Division of 0 <= x < 2^31 by a divisor known on the host: with l = ceil(log2 d)
+// and m = floor(2^(31 + l) / d) + 1, x m / 2^(31 + l) exceeds x / d by less than
+// x / 2^(31 + l) <= 1 / d, so its whole part is the quotient.
+struct Divisor {
+  unsigned m;
+  int shift;
+  __device__ __forceinline__ int div(int x) const {
+    return (int)(((unsigned long long)(unsigned)x * m) >> shift);
+  }
+};
+inline Divisor make_divisor(int d) {
+  int l = 0;
+  while ((1 << l) < d) ++l;
+  Divisor r;
+  r.m = (unsigned)((1ull << (31 + l)) / (unsigned)d + 1);
+  r.shift = 31 + l;
+  return r;
+}
+
+// Pairs of fp32 operations in one instruction.
+__device__ __forceinline__ uint64_t pair_of(float a, float b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ void pair_to(uint64_t v, float& a, float& b) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
 // ---------------------------------------------------------------------------
 // element types
 // ---------------------------------------------------------------------------
