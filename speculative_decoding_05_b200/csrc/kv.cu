@@ -8,6 +8,7 @@
 #include <cstdint>
 #include <type_traits>
 
+#include "attn_chunk.cuh"
 #include "attn_step.cuh"
 #include "kv_common.cuh"
 #include "kv_rows.cuh"
@@ -212,12 +213,33 @@ struct LaunchAttn {
     return st != DSPARK_OK ? st : join<T, TC, Dh>(N, p, ctas);
   }
 
+  template <typename T, int Dh>
+  dspark_status chunk() const {
+    constexpr int smem = (int)sizeof(ChunkSmem<Dh>) + 1024;
+    static_assert(smem <= kSmemLimit, "shared memory");
+    static DeviceOnce once;
+    set_smem_once(once, attn_chunk_kernel<T, Dh>, smem);
+    const int ctas = attn_sms();
+    const AttnParts p = parts(ctas, kChunkRows);
+    CUtensorMap mk, mv;
+    int box;
+    if (!maps<T, T>(&mk, &mv, kChunkKeys, &box)) return DSPARK_ERR_CUDA;
+    int box_shift = 0;
+    while (1 << box_shift < box) ++box_shift;
+    const dspark_status st =
+        launched(launch_dependent(attn_chunk_kernel<T, Dh>, dim3(ctas), dim3(kChunkThreads), smem,
+                                  s, a, p, mk, mv, box_shift));
+    return st != DSPARK_OK ? st : join<T, T, Dh>(kChunkRows, p, ctas);
+  }
+
   template <typename T, typename TC, int Dh>
   dspark_status run() {
+    if constexpr (sizeof(TC) != 1)
+      if (rows_per_head > 80) return chunk<T, Dh>();
     if (rows_per_head <= 16) return step<T, TC, Dh, 16>();
     if (rows_per_head <= 32) return step<T, TC, Dh, 32>();
     if constexpr (sizeof(TC) != 1)
-      if (rows_per_head > 64 && rows_per_head <= 80) return step<T, TC, Dh, 80>();
+      if (rows_per_head > 64) return step<T, TC, Dh, 80>();
     return step<T, TC, Dh, 64>();
   }
 };
@@ -347,7 +369,7 @@ dspark_status dspark_kv_read(
 
 size_t dspark_attn_workspace_size(int B, int Hq, int Hkv, int D, int max_len) {
   if (B < 0 || Hq <= 0 || Hkv <= 0 || Hq % Hkv != 0 || D <= 0 || max_len <= 0) return 0;
-  return part_bytes(kAttnMaxSms, 128, D).total;
+  return part_bytes(kAttnMaxSms, kChunkRows, D).total;
 }
 
 dspark_status dspark_attn_verify(
