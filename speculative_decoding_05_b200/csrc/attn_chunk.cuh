@@ -9,14 +9,17 @@
 //   S_p [128 rows, 128 keys] = Q_p K^T
 //   P_p = 2^(S_p - m), 16 bits, back to TMEM over S_p
 //   O_p [128 rows, D]       += P_p V      P from TMEM, V as it lies (MN-major)
-// with the MMAs in the order S0 S1 | PV0 S0' PV1 S1' | ..  A thread owns a row:
-// its maximum, sum and range checks need no other thread.  As in the step kernel
-// the reference m starts at 0 and moves only when a score leaves 2^+-kHot (fp16
-// weights: at the first tile), so that O is hardly ever rescaled.
+// with the MMAs in the order S0 S1 | PV0 S0' PV1 S1' | ..  A thread owns one row
+// of 64 keys: with all 128 a tile's softmax was a chain so long that the products
+// waited for it (4400 clocks a pair of tiles, 862 TFLOP/s).  The two threads of a
+// row share its reference m, which starts at 0 and moves only when a score leaves
+// 2^+-kHot (fp16 weights: at the first tile), as in the step kernel, so that O is
+// hardly ever rescaled; their two warps meet once a tile, to vote on that and
+// because the weights of one lie over the scores of the other.
 //
-// Warps: 8 softmax (two groups, a row tile each, which also load their Q rows),
-// one that loads K and V, one that issues the MMAs, one that clears V behind the
-// end of a sequence.
+// Warps: 16 softmax (two groups a row tile, which also load its Q rows), one that
+// loads K and V, one that issues the MMAs, one that clears V behind the end of a
+// sequence.
 #pragma once
 
 #include "attn_step.cuh"
@@ -25,7 +28,7 @@ namespace dspark {
 
 constexpr int kChunkRows = 256;
 constexpr int kChunkKeys = 128;
-constexpr int kChunkSoftmax = 8;  // warps
+constexpr int kChunkSoftmax = 16;  // warps
 constexpr int kChunkLoad = kChunkSoftmax;
 constexpr int kChunkMma = kChunkSoftmax + 1;
 constexpr int kChunkClean = kChunkSoftmax + 2;
@@ -38,6 +41,7 @@ struct ChunkSmem {
   static constexpr int kOps = D == 128 ? 4 : 8;
   alignas(1024) unsigned char op[kOps][kTile];
   alignas(1024) unsigned char q[2][128 * D * 2];
+  float part[2][2][128];  // of the two halves of each row tile's rows
   uint64_t full[kOps], empty[kOps];
   uint64_t q_full, s_full[2], p_full[2], o_full[2];
   uint64_t item_full[kChunkItems], item_empty[kChunkItems], v_clean[kChunkItems];
@@ -82,7 +86,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
     mbar_init(&sm.q_full, 32 * kChunkSoftmax);
     for (int i = 0; i < 2; ++i) {
       mbar_init(&sm.s_full[i], 1);
-      mbar_init(&sm.p_full[i], 128);
+      mbar_init(&sm.p_full[i], 256);
       mbar_init(&sm.o_full[i], 1);
     }
     for (int i = 0; i < kChunkItems; ++i) {
@@ -306,10 +310,14 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
     __syncwarp();
 
   } else {
-    // ---- softmax: a row a thread ----
-    const int p = warp >> 2, r = threadIdx.x & 127;
+    // ---- softmax: half of a row's keys a thread ----
+    const int p = warp >> 3, half = warp >> 2 & 1, r = threadIdx.x & 127;
+    constexpr int kMine = kChunkKeys / 2;  // keys of a thread
     const uint32_t lane_base = tmem + ((uint32_t)((warp & 3) * 32) << 16);
-    const uint32_t s_col = lane_base + p * 128, o_col = lane_base + kColO + p * D;
+    const uint32_t s_col = lane_base + p * 128 + half * kMine;
+    const uint32_t p_col = lane_base + p * 128 + half * (kMine / 2);
+    const uint32_t o_col = lane_base + kColO + p * D + half * (D / 2);
+    const int bar = 2 + p * 4 + (warp & 3);  // of the two warps with the same rows
     bool alive = true;
     auto wait = [&](uint64_t* bar, uint32_t parity) {
       if (alive && !mbar_wait(bar, parity)) {
@@ -337,7 +345,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
       const int rows = min(it.n_rows - p * 128, 128);
       constexpr int kC = D / 8;
 #pragma unroll 8
-      for (int i = r; i < 128 * kC; i += 128) {
+      for (int i = half * 128 + r; i < 128 * kC; i += 256) {
         const int x = i / kC, c = i % kC;
         const int rr = row_base + max(min(x, rows - 1), 0), tok = min(a.by_g.div(rr), it.n - 1);
         cp_async16(sm.q[p] + sw128_offset(x, 8 * c, 128),
@@ -364,7 +372,8 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
         const int k0 = (it.t0 + j) * kChunkKeys;
         const bool masked = k0 + kChunkKeys > pos_min + 1 || k0 < low_max;
         const bool first = j == 0 || k0 <= low_max;  // the first keys of some row
-        const int to = pos - k0, from = low - k0;    // keys of the tile that the row sees
+        // of this thread's keys the row sees [from, to]
+        const int to = pos - k0 - half * kMine, from = low - k0 - half * kMine;
         wait(&sm.s_full[p], (uint32_t)n_s & 1u);
         tc_fence_after();
         auto mask = [&](float (&x)[32], int c) {
@@ -372,7 +381,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
           for (int i = 0; i < 32; ++i)
             if (c + i > to || c + i < from) x[i] = -CUDART_INF_F;
         };
-        uint32_t w[kChunkKeys / 2];
+        uint32_t w[kMine / 2];
         bool raise = kHalf && first;
         float sum;
         while (true) {
@@ -380,7 +389,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
             // move the reference to the tile's maximum
             float top = -CUDART_INF_F;
 #pragma unroll 1
-            for (int c = 0; c < kChunkKeys; c += 32) {
+            for (int c = 0; c < kMine; c += 32) {
               float x[32];
               tmem_ld32(s_col + c, x);
 #pragma unroll
@@ -389,6 +398,9 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
 #pragma unroll
               for (int i = 0; i < 32; i += 2) top = max3(top, x[i], x[i + 1]);
             }
+            sm.part[p][half][r] = top;
+            named_sync(bar, 64);
+            top = fmaxf(top, sm.part[p][half ^ 1][r]);
             const float old = -neg_m;
             const bool seen = j > 0 && k0 > low;  // has keys before this tile
             const float now = seen ? fmaxf(old, top) : top == -CUDART_INF_F ? old : top;
@@ -397,7 +409,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
             l *= f;
             if (j > 0) {  // (the products up to tile j - 1 are done: S came behind them)
 #pragma unroll 1
-              for (int c = 0; c < D; c += 16) {
+              for (int c = 0; c < D / 2; c += 16) {
                 uint32_t o[16];
                 tmem_ld<16>(o_col + c, o);
 #pragma unroll
@@ -411,17 +423,15 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
           const uint64_t m2 = pair_of(neg_m, neg_m);
           float top = -CUDART_INF_F, bottom = CUDART_INF_F;
           uint64_t s2 = pair_of(0.0f, 0.0f), t2 = s2;
-          uint32_t raw[2][32];
-          tmem_ld32_issue(s_col, raw[0]);
 #pragma unroll
-          for (int c = 0; c < kChunkKeys; c += 32) {
-            uint32_t(&cur)[32] = raw[(c / 32) & 1];
-            tmem_ld32_wait(cur);
-            if (c + 32 < kChunkKeys) tmem_ld32_issue(s_col + c + 32, raw[(c / 32 + 1) & 1]);
+          for (int c = 0; c < kMine; c += 32) {
+            uint32_t raw[32];
+            tmem_ld32_issue(s_col + c, raw);
+            tmem_ld32_wait(raw);
             float x[32];
 #pragma unroll
             for (int i = 0; i < 32; i += 2)
-              pair_to(fma2(pair_of(__uint_as_float(cur[i]), __uint_as_float(cur[i + 1])), kf2, m2),
+              pair_to(fma2(pair_of(__uint_as_float(raw[i]), __uint_as_float(raw[i + 1])), kf2, m2),
                       x[i], x[i + 1]);
             if (masked) mask(x, c);
 #pragma unroll
@@ -443,13 +453,13 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
           float s0, s1;
           pair_to(add2(s2, t2), s0, s1);
           sum = s0 + s1;
-          if (raise) break;
-          raise = __any_sync(0xffffffffu, top > kHot || bottom < -kHot);
-          if (!raise) break;
+          // (both warps have read their scores when either goes on)
+          const bool hot = vote_any(bar, 64, top > kHot || bottom < -kHot);
+          if (raise || !hot) break;
+          raise = true;
         }
         l += sum;
-        tmem_st32(s_col, *reinterpret_cast<uint32_t(*)[32]>(&w[0]));
-        tmem_st32(s_col + 32, *reinterpret_cast<uint32_t(*)[32]>(&w[32]));
+        tmem_st32(p_col, w);
         tmem_st_wait();
         tc_fence_before();
         mbar_arrive(&sm.p_full[p]);
@@ -462,14 +472,17 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
         tc_fence_after();
       }
       const bool whole = it.part == 0;
+      sm.part[p][half][r] = l;
+      named_sync(bar, 64);
+      l = sm.part[p][0][r] + sm.part[p][1][r];
       const float inv = 1.0f / l;
       float worst = 0.0f;
       const size_t slot_row =
           (size_t)(2 * blockIdx.x + (it.part == 2)) * kChunkRows + p * 128 + r;
       T* out = static_cast<T*>(a.out) +
-               ((it.row0 + tok) * a.Hq + it.h * a.G + rr - tok * a.G) * D;
+               ((it.row0 + tok) * a.Hq + it.h * a.G + rr - tok * a.G) * D + half * (D / 2);
 #pragma unroll 1
-      for (int c = 0; c < D; c += 32) {
+      for (int c = 0; c < D / 2; c += 32) {
         float o[32];
         if (nt > 0) {
           tmem_ld32(o_col + c, o);
@@ -493,16 +506,18 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
         } else if (r < rows) {
 #pragma unroll
           for (int i = 0; i < 32; i += 4)
-            *reinterpret_cast<float4*>(parts.o + slot_row * D + c + i) =
+            *reinterpret_cast<float4*>(parts.o + slot_row * D + half * (D / 2) + c + i) =
                 make_float4(o[i], o[i + 1], o[i + 2], o[i + 3]);
         }
       }
       // a part without a visible key has no reference
-      if (!whole && r < rows)
+      if (!whole && r < rows && half == 0)
         parts.ml[slot_row] = make_float2(l == 0.0f ? -CUDART_INF_F : -neg_m, l);
       tc_fence_before();
       // a result that is not finite may come from a position that its row does
       // not see (0 times infinity): form the row again from those it sees
+      // (both warps of the row: its other half is stored by then)
+      named_sync(bar, 64);
       unsigned bad = __ballot_sync(0xffffffffu, whole && r < rows && worst != 0.0f);
       while (bad) {
         const int src = __ffs(bad) - 1;
