@@ -104,7 +104,11 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
   grid_dep_launch();
   grid_dep_wait();
   tc_fence_before();
-  find_piece<kChunkThreads>(a, tiles, sm.scan, &sm.piece, flags);  // syncs the block
+  const bool small = a.rows.B <= 32;
+  if (small)
+    __syncthreads();
+  else
+    find_piece<kChunkThreads>(a, tiles, sm.scan, &sm.piece, flags);  // syncs the block
   tc_fence_after();
   const uint32_t tmem = sm.tmem;
 
@@ -113,7 +117,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
     const int shift = a.rows.page_shift, in_page = (1 << shift) - 1;
     const int box_rows = 1 << box_shift;
     Walk walk;
-    walk.start(a, tiles, sm.piece);
+    walk.start(a, tiles, small ? find_piece_warp(a, tiles, flags) : sm.piece);
     PartRecord rec = {};
     rec.b = -1;
     int op = 0;

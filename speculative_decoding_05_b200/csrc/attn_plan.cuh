@@ -68,6 +68,80 @@ struct Piece {
   int b, h, qt, n, past;
 };
 
+// The piece that starts at `start`, in request b (of the given length, rows and
+// cost a head) whose first item starts at `at`.
+__device__ __forceinline__ void set_piece(const AttnArgs& a, const AttnTiles& t, Piece* p, int b,
+                                          int n, int past, long long row0, long long head,
+                                          long long start, long long at, long long len) {
+  long long off = start - at;
+  const int h = (int)quotient(off, head);
+  off -= h * head;
+  int qt = 0, lo;
+  while (true) {
+    const int ic = item_tiles(t, a, n, past, qt, lo) + kItemCost;
+    if (off < ic) break;
+    off -= ic;
+    ++qt;
+  }
+  p->b = b;
+  p->h = h;
+  p->qt = qt;
+  p->n = n;
+  p->past = past;
+  p->row0 = row0;
+  p->off = off;
+  p->len = len;
+}
+// Start and length of this CTA's piece of a line of `total`: equal pieces, the
+// first ones longer by one; false if it has none.
+__device__ __forceinline__ bool cut_line(long long total, long long& start, long long& len) {
+  long long ctas = total / kMinPiece;
+  if (ctas > gridDim.x) ctas = gridDim.x;
+  if (ctas < 1) ctas = 1;
+  const long long c = blockIdx.x;
+  if (c >= ctas) return false;
+  const long long each = quotient(total, ctas), more = total - each * ctas;
+  start = c * each + min(c, more);
+  len = each + (c < more);
+  return len > 0;
+}
+
+// This CTA's piece of the line by one warp, for up to 32 requests: no thread of
+// the block waits for another (a short call's first loads come 1 us earlier).
+__device__ __forceinline__ Piece find_piece_warp(const AttnArgs& a, const AttnTiles& t,
+                                                 unsigned& flags) {
+  const KvRows& r = a.rows;
+  const int lane = threadIdx.x & 31;
+  int past = 0, n = 0;
+  long long row0 = 0, head = 0;
+  if (lane < r.B) {
+    past = r.cache_len[lane];
+    row0 = r.row_start[lane];
+    n = checked_new(r, lane, past, row0, flags);
+    if (n) head = head_cost(t, a, n, past);
+  }
+  const long long mine = a.Hkv * head;
+  long long incl = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long v = __shfl_up_sync(0xffffffffu, incl, o);
+    if (lane >= o) incl += v;
+  }
+  const long long total = __shfl_sync(0xffffffffu, incl, 31);
+  Piece p = {};
+  long long start = 0, len = 0;
+  if (!cut_line(total, start, len)) return p;
+  const unsigned upto = __ballot_sync(0xffffffffu, incl > start);
+  const int b = __ffs(upto) - 1;  // (start < total: there is one)
+  n = __shfl_sync(0xffffffffu, n, b);
+  past = __shfl_sync(0xffffffffu, past, b);
+  row0 = __shfl_sync(0xffffffffu, row0, b);
+  head = __shfl_sync(0xffffffffu, head, b);
+  const long long at = __shfl_sync(0xffffffffu, incl - mine, b);
+  set_piece(a, t, &p, b, n, past, row0, head, start, at, len);
+  return p;
+}
+
 // This CTA's piece of the line, by the NT threads of the block.
 template <int NT>
 __device__ __forceinline__ void find_piece(const AttnArgs& a, const AttnTiles& t,
@@ -106,42 +180,16 @@ __device__ __forceinline__ void find_piece(const AttnArgs& a, const AttnTiles& t
     if (i < w) pre += v;
     total += v;
   }
-  long long ctas = total / kMinPiece;
-  if (ctas > gridDim.x) ctas = gridDim.x;
-  if (ctas < 1) ctas = 1;
-  const long long c = blockIdx.x;
-  if (c < ctas) {
-    // equal pieces, the first total % ctas of them longer by one
-    const long long len = quotient(total, ctas), more = total - len * ctas;
-    const long long start = c * len + min(c, more);
-    const long long mylen = len + (c < more);
-    if (mylen > 0 && start >= pre && start < pre + mine) {
-      long long at = pre;
-      for (int b = b0; b < b1; ++b) {
-        const long long k = per == 1 ? mine : request(b);
-        if (start < at + k) {
-          long long off = start - at;
-          const int h = (int)quotient(off, head);
-          off -= h * head;
-          int qt = 0, lo;
-          while (true) {
-            const int ic = item_tiles(t, a, n, past, qt, lo) + kItemCost;
-            if (off < ic) break;
-            off -= ic;
-            ++qt;
-          }
-          s_piece->b = b;
-          s_piece->h = h;
-          s_piece->qt = qt;
-          s_piece->n = n;
-          s_piece->past = past;
-          s_piece->row0 = row0;
-          s_piece->off = off;
-          s_piece->len = mylen;
-          break;
-        }
-        at += k;
+  long long start = 0, len = 0;
+  if (cut_line(total, start, len) && start >= pre && start < pre + mine) {
+    long long at = pre;
+    for (int b = b0; b < b1; ++b) {
+      const long long k = per == 1 ? mine : request(b);
+      if (start < at + k) {
+        set_piece(a, t, s_piece, b, n, past, row0, head, start, at, len);
+        break;
       }
+      at += k;
     }
   }
   __syncthreads();
@@ -253,6 +301,7 @@ __host__ inline PartBytes part_bytes(int ctas, int rows, int D) {
 }
 
 constexpr int kJoinThreads = 256;
+constexpr int kJoinPerSm = 4;  // blocks: a row is a chain of loads, more rows at a time hide it
 constexpr int kMaxAttnCtas = 256;
 
 // Joins the parts of split items: out = sum_i 2^(m_i - M) o_i / sum_i
@@ -261,7 +310,7 @@ constexpr int kMaxAttnCtas = 256;
 // it.  A warp a row; the rows of all split items are one line, dealt out over
 // all warps (few items have many rows and parts, many have few).
 template <typename T, typename TC, int D>
-__global__ void __launch_bounds__(kJoinThreads)
+__global__ void __launch_bounds__(kJoinThreads, kJoinPerSm)
     attn_join_kernel(const AttnArgs a, const int tile_rows, const AttnParts p, const int ctas) {
   constexpr int E = D / 32;  // elements of a lane
   using V = typename std::conditional<E == 4, float4, float2>::type;
@@ -283,7 +332,7 @@ __global__ void __launch_bounds__(kJoinThreads)
 #pragma unroll
     for (int e = 0; e < E; ++e) o[e] = 0.0f;
     // parts in batches, so that their loads overlap
-    constexpr int kBatch = 8;
+    constexpr int kBatch = 6;
     int c = c0;
     bool more = true;
     while (more) {

@@ -208,7 +208,11 @@ __global__ void __launch_bounds__(step_threads<TC>(), 1)
   grid_dep_launch();
   grid_dep_wait();
   tc_fence_before();
-  find_piece<kThreads>(a, tiles, sm.scan, &sm.piece, flags);  // syncs the block
+  const bool small = a.rows.B <= 32;
+  if (small)
+    __syncthreads();
+  else
+    find_piece<kThreads>(a, tiles, sm.scan, &sm.piece, flags);  // syncs the block
   tc_fence_after();
   const uint32_t tmem = sm.tmem;
   if constexpr (!kQ8) {
@@ -232,7 +236,7 @@ __global__ void __launch_bounds__(step_threads<TC>(), 1)
     volatile int* my_next = is_k ? &sm.next_k : &sm.next_v;
     const volatile int* other_next = is_k ? &sm.next_v : &sm.next_k;
     Walk walk;
-    if (is_k) walk.start(a, tiles, sm.piece);
+    if (is_k) walk.start(a, tiles, small ? find_piece_warp(a, tiles, flags) : sm.piece);
     PartRecord rec = {};
     rec.b = -1;
     int op0 = 0, tile0 = 0;

@@ -190,7 +190,7 @@ struct LaunchAttn {
 
   template <typename T, typename TC, int Dh>
   dspark_status join(int tile_rows, const AttnParts& p, int ctas) const {
-    return launched(launch_dependent(attn_join_kernel<T, TC, Dh>, dim3(2 * attn_sms()),
+    return launched(launch_dependent(attn_join_kernel<T, TC, Dh>, dim3(kJoinPerSm * attn_sms()),
                                      dim3(kJoinThreads), 0, s, a, tile_rows, p, ctas));
   }
 
