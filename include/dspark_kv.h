@@ -41,12 +41,13 @@
  * defined; a scale that is not finite makes the row's values not finite.
  *
  * Sizes: D 64 or 128; page_size 16, 32, 64, 128 or 256; B <= 4096; Hq a
- * multiple of Hkv, Hq <= 1024; n_pages * Hkv * page_size < 2^31.  Everything
+ * multiple of Hkv, Hq <= 1024; n_pages * Hkv * page_size < 2^31; n_rows and
+ * n_rows * Hq < 2^31; positions below 2^30 (later ones: see below).  Everything
  * 16-byte aligned (the workspace 256); row strides (in elements) multiples
  * of 8, the heads of a row contiguous.  Other sizes: DSPARK_ERR_UNSUPPORTED.
  *
  * Data errors.  A request with verify_len outside its range, rows outside
- * [0, n_rows) or positions outside [0, max_pages * page_size) raises
+ * [0, n_rows) or positions outside [0, max_pages * page_size) or past 2^30 raises
  * DSPARK_FLAG_BAD_LENGTH and is treated as idle.  A page id outside
  * [0, n_pages) raises DSPARK_FLAG_BAD_PAGE; nothing is written there and
  * reads take page 0 instead.

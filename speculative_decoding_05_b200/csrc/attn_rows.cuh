@@ -44,10 +44,16 @@ __device__ __noinline__ void attend_row(const AttnArgs& a, int b, int pos, int h
     o[e] = o[e + 1] = 0.0f;
   }
   float m = -CUDART_INF_F, sum = 0.0f;
+  // a query with a value that is not finite has scores that are not finite, all
+  // of them: no softmax
+  float q_odd = 0.0f;
+#pragma unroll
+  for (int e = 0; e < E; ++e) q_odd = fmaf(q[e], 0.0f, q_odd);
+  if (__any_sync(0xffffffffu, q_odd != 0.0f)) sum = CUDART_NAN_F;
   int page = 0;
   const int mask = (1 << r.page_shift) - 1;
   const int j0 = first_seen(pos, a.window);
-  for (int j = j0; j <= pos; ++j) {
+  for (int j = j0; j <= pos && sum == sum; ++j) {  // (a sum that is no number stays so)
     if (j == j0 || (j & mask) == 0) {
       page = checked_page(r, b, j >> r.page_shift, flags);
       if (page < 0) page = 0;

@@ -99,7 +99,7 @@ KvRows make_rows(const Common& c, int max_len) {
   r.page_table = c.page_table;
   r.n_rows = c.n_rows;
   r.max_pos = (long long)c.max_pages * c.page_size;
-  if (r.max_pos > (1ll << 31) - 1) r.max_pos = (1ll << 31) - 1;  // positions are int32
+  if (r.max_pos > 1ll << 30) r.max_pos = 1ll << 30;  // positions and tile ends are int32
   r.B = c.B;
   r.max_len = max_len;
   r.max_pages = c.max_pages;

@@ -497,11 +497,11 @@ def dspark_kv_append(q, k, v, row_start, verify_len, cache_len, page_table, k_ca
         rot = 2 * inv_freq.numel()
         _kv_want("inv_freq", inv_freq, (rot // 2,), torch.float64, dev)
     _kv_call(load().dspark_kv_append, dev, workspace, stream,
-             (q.data_ptr(), k.data_ptr(), v.data_ptr(), qs, ks, vs, act, n_rows, B, Hq, Hkv, D, row_start.data_ptr(),
-              verify_len.data_ptr(), cache_len.data_ptr(), page_table.data_ptr(), max_pages, k_cache.data_ptr(),
-              v_cache.data_ptr(), _at(k_scale), _at(v_scale), code, n_pages, ps, _at(q_norm),
-              _at(k_norm), eps, _at(inv_freq), rot, int(bool(interleaved)), rope_scale,
-              q_out.data_ptr()))
+             (q.data_ptr(), k.data_ptr(), v.data_ptr(), qs, ks, vs, act, n_rows, B, Hq, Hkv, D,
+              row_start.data_ptr(), verify_len.data_ptr(), cache_len.data_ptr(),
+              page_table.data_ptr(), max_pages, k_cache.data_ptr(), v_cache.data_ptr(),
+              _at(k_scale), _at(v_scale), code, n_pages, ps, _at(q_norm), _at(k_norm), eps,
+              _at(inv_freq), rot, int(bool(interleaved)), rope_scale, q_out.data_ptr()))
 
 
 def dspark_kv_read(k_cache, v_cache, row_start, verify_len, cache_len, page_table, k_out, v_out,
@@ -514,9 +514,10 @@ def dspark_kv_read(k_cache, v_cache, row_start, verify_len, cache_len, page_tabl
     _kv_want("k_out", k_out, (n_rows, Hkv, D), k_out.dtype, dev)
     _kv_want("v_out", v_out, (n_rows, Hkv, D), k_out.dtype, dev)
     _kv_call(load().dspark_kv_read, dev, workspace, stream,
-             (k_cache.data_ptr(), v_cache.data_ptr(), _at(k_scale), _at(v_scale), code, n_pages, ps,
-              row_start.data_ptr(), verify_len.data_ptr(), cache_len.data_ptr(), page_table.data_ptr(), max_pages, n_rows,
-              B, Hkv, D, k_out.data_ptr(), v_out.data_ptr(), _kv_type(k_out, "k_out")))
+             (k_cache.data_ptr(), v_cache.data_ptr(), _at(k_scale), _at(v_scale), code, n_pages,
+              ps, row_start.data_ptr(), verify_len.data_ptr(), cache_len.data_ptr(),
+              page_table.data_ptr(), max_pages, n_rows, B, Hkv, D, k_out.data_ptr(),
+              v_out.data_ptr(), _kv_type(k_out, "k_out")))
 
 
 def dspark_attn_workspace_size(B, Hq, Hkv, D, max_len) -> int:
@@ -535,7 +536,7 @@ def dspark_attn_verify(q, k_cache, v_cache, row_start, verify_len, cache_len, pa
     Hq, qs = _kv_rows("q", q, n_rows, D, dev, q.dtype)
     _kv_want("out", out, (n_rows, Hq, D), q.dtype, dev)
     _kv_call(load().dspark_attn_verify, dev, workspace, stream,
-             (q.data_ptr(), qs, act, n_rows, B, Hq, Hkv, D, max_len, row_start.data_ptr(), verify_len.data_ptr(),
-              cache_len.data_ptr(), page_table.data_ptr(), max_pages, k_cache.data_ptr(), v_cache.data_ptr(),
-              _at(k_scale), _at(v_scale), code, n_pages, ps,
-              D ** -0.5 if sm_scale is None else sm_scale, window, out.data_ptr()))
+             (q.data_ptr(), qs, act, n_rows, B, Hq, Hkv, D, max_len, row_start.data_ptr(),
+              verify_len.data_ptr(), cache_len.data_ptr(), page_table.data_ptr(), max_pages,
+              k_cache.data_ptr(), v_cache.data_ptr(), _at(k_scale), _at(v_scale), code, n_pages,
+              ps, D ** -0.5 if sm_scale is None else sm_scale, window, out.data_ptr()))

@@ -283,3 +283,41 @@ def test_many_short_items_back_to_back(cache, D_, G, n):
     torch.cuda.synchronize()
     for o in outs:
         assert torch.equal(o, first)
+
+
+@pytest.mark.parametrize("cache", [BF, E4])
+@pytest.mark.parametrize("n", [5, 150])
+def test_queries_that_are_not_finite_spoil_their_own_rows_only(cache, n):
+    """A NaN or an infinity in a query head: that row and head is not a number,
+    every other result holds."""
+    p = Problem([n, 2], [300, 60], 8, 2, 128, BF, cache, 64, seed=24)
+    ref = attention(p)
+    bad = [(p.start[0] + 1, 3, float("nan")), (p.start[0] + 2, 6, float("inf")),
+           (p.start[1], 0, -float("inf"))]
+    for row, h, x in bad:
+        p.q[row, h, 17] = x
+    out, ws = attend(p)
+    torch.cuda.synchronize()
+    assert D.dspark_get_device_flags(ws) == 0
+    for row, h, _ in bad:
+        assert bool(torch.isnan(out[row, h].float()).all())
+    for rows, want, tol in ref:
+        got = out[rows].double()
+        err = (got - want).abs() <= tol
+        for row, h, _ in bad:
+            if rows.start <= row < rows.stop:
+                err[row - rows.start, h] = True
+        # (the e4m3 parts of the other rows formed with a bad one: rows one by one)
+        assert bool(err.all())
+
+
+def test_positions_past_the_limit_are_flagged():
+    """A table that repeats one page reaches positions that no tile end can hold."""
+    p = Problem([3, 2], [40, 50], 8, 2, 128, page=256, seed=25, max_pages=(1 << 22) + 4)
+    ref = attention(p)
+    p.page_table[0] = 0
+    p.cache_len[0] = (1 << 30) - 2
+    out, ws = attend(p)
+    torch.cuda.synchronize()
+    assert D.dspark_get_device_flags(ws) == D.FLAG_BAD_LENGTH
+    check(p, out, ref[1:])
