@@ -85,6 +85,14 @@ __device__ __forceinline__ float group_max(float v, int lanes) {
   return v;
 }
 
+// Place of the cosine and sine of pair i among rot / 2 = half: the even groups of
+// four first, then the odd ones, so that lanes that read two groups each (8
+// pairs behind each other) meet no bank twice.
+__device__ __forceinline__ int angle_place(int i, int half) {
+  const int c = i >> 2;
+  return ((c & 1) * (half >> 3) + (c >> 1)) * 4 + (i & 3);
+}
+
 // One kind of vectors of a run of tokens: heads [0, H) of the rows at `src`,
 // normed by w (or NULL) and turned if `turn`, to q_out (kOut) or the cache.
 // Eight elements of a lane as four pairs.
@@ -104,7 +112,7 @@ __device__ __forceinline__ void append_heads(const AppendArgs& a, const TokenPla
   const bool first = 8 * l < half;
   int mate = threadIdx.x & 31, angle = 0;
   if (mine) {
-    angle = a.interleaved ? 4 * l : first ? 8 * l : 8 * l - half;
+    angle = angle_place(a.interleaved ? 4 * l : first ? 8 * l : 8 * l - half, half);
     if (!a.interleaved) mate += first ? half / 8 : -(half / 8);
   }
   uint64_t wv[4];
@@ -177,8 +185,9 @@ __device__ __forceinline__ void append_heads(const AppendArgs& a, const TokenPla
           if (mine) {
 #pragma unroll
             for (int j = 0; j < 4; j += 2) {
-              const float4 c = *reinterpret_cast<const float4*>(co + 2 * j);
-              float4 s = *reinterpret_cast<const float4*>(si + 2 * j);
+              const int at = j / 2 * (half / 2);  // the odd group
+              const float4 c = *reinterpret_cast<const float4*>(co + at);
+              float4 s = *reinterpret_cast<const float4*>(si + at);
               if (first) s = make_float4(-s.x, -s.y, -s.z, -s.w);
               x[j] = fma2(x[j], pair_of(c.x, c.y), mul2(other[j], pair_of(s.x, s.y)));
               x[j + 1] = fma2(x[j + 1], pair_of(c.z, c.w), mul2(other[j + 1], pair_of(s.z, s.w)));
@@ -274,8 +283,9 @@ __global__ void __launch_bounds__(kRowThreads, 4) kv_append_kernel(const AppendA
       const double turn = (double)s_tok[tok].pos * a.inv_freq[i] * 0.15915494309189533577;
       float s, c;
       sincospif(2.0f * (float)(turn - rint(turn)), &s, &c);
-      s_cos[tok * (D / 2) + i] = c * a.rope_scale;
-      s_sin[tok * (D / 2) + i] = s * a.rope_scale;
+      const int at = tok * (D / 2) + angle_place(i, half);
+      s_cos[at] = c * a.rope_scale;
+      s_sin[at] = s * a.rope_scale;
     }
     if (half > 0) __syncthreads();
     append_heads<T, TC, D, false>(a, s_tok, s_cos, s_sin, n_tok, a.Hkv, a.by_hkv, a.k, a.k_stride,
