@@ -41,8 +41,9 @@
  * defined; a scale that is not finite makes the row's values not finite.
  *
  * Sizes: D 64 or 128; page_size 16, 32, 64, 128 or 256; B <= 4096; Hq a
- * multiple of Hkv, Hq <= 1024; n_pages * Hkv * page_size < 2^31; n_rows and
- * n_rows * Hq < 2^31; positions below 2^30 (later ones: see below).  Everything
+ * multiple of Hkv, Hq <= 1024; n_pages * Hkv * page_size < 2^31; n_rows at
+ * most 2^31 - 2^16, in the attention n_rows * Hq < 2^31; positions below 2^30
+ * (later ones: see below).  Everything
  * 16-byte aligned (the workspace 256); row strides (in elements) multiples
  * of 8, the heads of a row contiguous.  Other sizes: DSPARK_ERR_UNSUPPORTED.
  *
@@ -137,7 +138,10 @@ size_t dspark_attn_workspace_size(int B, int Hq, int Hkv, int D, int max_len);
  * Scores, softmax statistics and sums are fp32; the weights are rounded to 16
  * bits (the value rows' type; fp16 with an e4m3 cache) for the product with
  * V; out is rounded once.  Positions a row does not see never reach it: K and
- * V there may hold anything, infinities and NaN included.
+ * V there may hold anything, infinities and NaN included.  A row whose result is
+ * not finite is formed again by itself: right, but slow.  (Over more than 2^19
+ * positions such rows may hold a step's CTA up for longer than its waits' limit
+ * of 2 s: the call then ends with DSPARK_FLAG_TIMEOUT.)
  *
  * Inputs   q [n_rows, Hq, D] act_dtype, rows q_stride elements apart;
  *          max_len: an upper bound of verify_len + 1, at least 1 (K + 1 of a

@@ -41,7 +41,7 @@ struct ChunkSmem {
   static constexpr int kOps = D == 128 ? 4 : 8;
   alignas(1024) unsigned char op[kOps][kTile];
   alignas(1024) unsigned char q[2][128 * D * 2];
-  float part[2][2][128];  // of the two halves of each row tile's rows
+  float part[2][2][128], odd[2][2][128];  // of the two halves of each row tile's rows
   uint64_t full[kOps], empty[kOps];
   uint64_t q_full, s_full[2], p_full[2], o_full[2];
   uint64_t item_full[kChunkItems], item_empty[kChunkItems], v_clean[kChunkItems];
@@ -51,6 +51,7 @@ struct ChunkSmem {
   long long scan[kChunkThreads / 32 + 1];
   uint32_t tmem;
   unsigned flags;
+  int slow;  // see mbar_wait_slow
   int stop, last, next;
 };
 
@@ -60,6 +61,29 @@ __device__ __forceinline__ int chunk_tiles(const AttnArgs& a, const Item& it, in
   const int r = it.qt * kChunkRows + min(128 * (p + 1), it.n_rows) - 1;
   const int n = (it.past + a.by_g.div(r)) / kChunkKeys + 1;
   return max(min(it.t1, n) - it.t0, 0);
+}
+
+// Waits of this kernel, whose softmax warps may be held up by attend_row: it ends,
+// but where all rows of a long sequence need it a CTA takes seconds.  `slow` counts
+// the warps that went into it and have not done an item's tiles since, and a
+// wait's limit runs anew while there are any.  The softmax warps' own waits have
+// the plain limit (they start an item together, when none is in attend_row any
+// more), so these end as well.  (The step kernel has a fifth of the rows, and its
+// e4m3 form lost 7 % to these few instructions: plain waits there.)
+template <typename F>
+__device__ __forceinline__ bool wait_slow(const volatile int* slow, F&& wait) {
+  do {
+    if (wait()) return true;
+  } while (*slow);
+  return false;
+}
+__device__ __forceinline__ bool mbar_wait_slow(const volatile int* slow, uint64_t* bar,
+                                               uint32_t parity) {
+  return wait_slow(slow, [&] { return mbar_wait(bar, parity); });
+}
+__device__ __forceinline__ void count_slow(int* slow, int by) {
+  __syncwarp();
+  if ((threadIdx.x & 31) == 0) atomicAdd(slow, by);
 }
 
 template <typename T, int D>
@@ -96,6 +120,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
     }
     mbar_init(&sm.drain, 1);
     sm.flags = 0;
+    sm.slow = 0;
     sm.last = -1;
     sm.next = 0;
     fence_barrier_init();
@@ -126,7 +151,8 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
       const int slot = n_item % kChunkItems;
       const Item it = walk.next(a, tiles);
       if (n_item >= kChunkItems)
-        alive = mbar_wait(&sm.item_empty[slot], (uint32_t)(n_item / kChunkItems - 1) & 1u);
+        alive = mbar_wait_slow(&sm.slow, &sm.item_empty[slot],
+                               (uint32_t)(n_item / kChunkItems - 1) & 1u);
       if (!__all_sync(0xffffffffu, alive)) {
         alive = false;
         break;
@@ -170,7 +196,8 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
 #pragma unroll 1
         for (int kv = 0; kv < 2; ++kv, ++op) {
           const int stage = op % kOps;
-          if (op >= kOps) alive = mbar_wait(&sm.empty[stage], (uint32_t)(op / kOps - 1) & 1u);
+          if (op >= kOps)
+            alive = mbar_wait_slow(&sm.slow, &sm.empty[stage], (uint32_t)(op / kOps - 1) & 1u);
           if (!__all_sync(0xffffffffu, alive)) {
             alive = false;
             break;
@@ -206,7 +233,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
     int op0 = 0;
     for (int n_item = 0;; ++n_item) {
       const int slot = n_item % kChunkItems;
-      alive = mbar_wait(&sm.item_full[slot], (uint32_t)(n_item / kChunkItems) & 1u);
+      alive = mbar_wait_slow(&sm.slow, &sm.item_full[slot], (uint32_t)(n_item / kChunkItems) & 1u);
       if (!__all_sync(0xffffffffu, alive)) {
         alive = false;
         break;
@@ -218,8 +245,8 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
       if (has_tail(it)) {
         const int use = op0 + 2 * (it.t1 - it.t0) - 1, stage = use % kOps;
         // once it is issued, the parity can mean this fill only
-        alive = next_past(&sm.next, use) &&
-                mbar_wait(&sm.full[stage], (uint32_t)(use / kOps) & 1u);
+        alive = wait_slow(&sm.slow, [&] { return next_past(&sm.next, use); }) &&
+                mbar_wait_slow(&sm.slow, &sm.full[stage], (uint32_t)(use / kOps) & 1u);
         if (!__all_sync(0xffffffffu, alive)) {
           alive = false;
           break;
@@ -246,7 +273,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
     if (elect_one()) {
       bool alive = true;
       auto wait = [&](uint64_t* bar, uint32_t parity) {
-        if (alive) alive = mbar_wait_spin(bar, parity);
+        if (alive) alive = wait_slow(&sm.slow, [&] { return mbar_wait_spin(bar, parity); });
       };
       int op0 = 0, n_s[2] = {0, 0};  // operands and P tiles before the item
       for (int n_item = 0;; ++n_item) {
@@ -330,6 +357,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
       }
     };
     int n_s = 0, n_o = 0;
+    bool was_slow = false;  // attend_row at the item before
     const uint64_t kf2 = pair_of(a.scale2, a.scale2);
     for (int n_item = 0;; ++n_item) {
       const int slot = n_item % kChunkItems;
@@ -468,6 +496,8 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
         tc_fence_before();
         mbar_arrive(&sm.p_full[p]);
       }
+      if (was_slow) count_slow(&sm.slow, -1);
+      was_slow = false;
 
       // ---- the item's rows ----
       if (nt > 0) {
@@ -520,14 +550,21 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
       tc_fence_before();
       // a result that is not finite may come from a position that its row does
       // not see (0 times infinity): form the row again from those it sees
-      // (both warps of the row: its other half is stored by then)
+      // (the row's two warps take such rows in turn; both halves are stored by then)
+      sm.odd[p][half][r] = worst;
       named_sync(bar, 64);
-      unsigned bad = __ballot_sync(0xffffffffu, whole && r < rows && worst != 0.0f);
-      while (bad) {
-        const int src = __ffs(bad) - 1;
-        bad &= bad - 1;
-        const int rb = __shfl_sync(0xffffffffu, rr, src), tb = a.by_g.div(rb);
-        attend_row<T, T, D>(a, it.b, it.past + tb, it.h * a.G + rb - tb * a.G, it.row0 + tb, flags);
+      unsigned bad = __ballot_sync(
+          0xffffffffu, whole && r < rows && (worst != 0.0f || sm.odd[p][half ^ 1][r] != 0.0f));
+      if (bad) {
+        count_slow(&sm.slow, 1);
+        was_slow = true;
+        for (int i = 0; bad; bad &= bad - 1, ++i) {
+          const int src = __ffs(bad) - 1;
+          const int rb = __shfl_sync(0xffffffffu, rr, src), tb = a.by_g.div(rb);
+          if ((i & 1) == half)
+            attend_row<T, T, D>(a, it.b, it.past + tb, it.h * a.G + rb - tb * a.G, it.row0 + tb,
+                                flags);
+        }
       }
     }
   }

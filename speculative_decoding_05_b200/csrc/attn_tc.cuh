@@ -203,8 +203,9 @@ __device__ __forceinline__ uint2 widen4(uint32_t c) {
 // An e4m3 tile of 128 rows x D bytes (as TMA wrote it, swizzled over its row) to
 // fp16 in the operands' layout (64-element halves, 128-byte swizzle), by 128
 // threads; rows from `rows` on become zero: what lies behind a sequence may be
-// anything, and 0 times a NaN is none.  (Loops kept short: the warps of a CTA run different code, and what
-// does not fit the instruction cache of an SM's quarter costs more than it saves.)
+// anything, and 0 times a NaN is none.  (Loops kept short: the warps of a CTA run
+// different code, and what does not fit the instruction cache of an SM's quarter
+// costs more than it saves.)
 template <int D>
 __device__ __forceinline__ void widen_tile(const unsigned char* raw, unsigned char* op, int rows,
                                            int tid) {
@@ -217,8 +218,7 @@ __device__ __forceinline__ void widen_tile(const unsigned char* raw, unsigned ch
   for (int i0 = tid; i0 < 128 * kChunks; i0 += 128 * kBatch) {
     uint4 u[kBatch];
 #pragma unroll
-    for (int b = 0; b < kBatch; ++b)
-    {
+    for (int b = 0; b < kBatch; ++b) {
       const int row = (i0 + 128 * b) / kChunks;
       u[b] = *reinterpret_cast<const uint4*>(raw + k8_offset<D>(row, 16 * c));
       if (row >= rows) u[b] = make_uint4(0, 0, 0, 0);

@@ -70,7 +70,7 @@ dspark_status check_common(const Common& c) {
   if (c.Hq % c.Hkv != 0) return DSPARK_ERR_INVALID_ARG;
   if ((c.D != 64 && c.D != 128) || page_shift(c.page_size) < 0 || c.B > kKvMaxB || c.Hq > 1024)
     return DSPARK_ERR_UNSUPPORTED;
-  if (c.n_rows >= (1ll << 31) || c.n_pages >= (1ll << 31) ||
+  if (c.n_rows > kKvMaxRows || c.n_pages >= (1ll << 31) ||
       c.n_pages * c.Hkv * c.page_size >= (1ll << 31))
     return DSPARK_ERR_UNSUPPORTED;
   if (!c.ws || !aligned(c.ws, 256) || c.ws_bytes < c.ws_need) return DSPARK_ERR_WORKSPACE;

@@ -41,6 +41,7 @@ __device__ __forceinline__ void store_status(unsigned* ws, unsigned flags) {
 // ---------------------------------------------------------------------------
 
 constexpr int kKvMaxB = 4096;
+constexpr long long kKvMaxRows = (1ll << 31) - (1 << 16);  // a step past them stays an int32
 
 struct KvRows {  // the row markers (dspark_kv.h, "Rows")
   const int64_t* row_start;

@@ -257,7 +257,8 @@ __global__ void __launch_bounds__(kRowThreads, 4) kv_append_kernel(const AppendA
   scan_requests<kRowThreads>(r.B, s_first, s_warp, [&](int b) {
     return checked_new(r, b, r.cache_len[b], r.row_start[b], flags);
   });
-  const int total = s_first[r.B];
+  // (rows that overlap against the rules may add up to anything)
+  const int total = min(max(s_first[r.B], 0), (int)r.n_rows);
   const int run = run_length(total);
   const int half = a.rot / 2;
   for (int i0 = blockIdx.x * run; i0 < total; i0 += gridDim.x * run) {
@@ -320,7 +321,8 @@ __global__ void __launch_bounds__(kRowThreads) kv_read_kernel(const ReadArgs a) 
   scan_requests<kRowThreads>(r.B, s_first, s_warp, [&](int b) {
     return checked_new(r, b, r.cache_len[b], r.row_start[b], flags);
   });
-  const int total = s_first[r.B];
+  // (rows that overlap against the rules may add up to anything)
+  const int total = min(max(s_first[r.B], 0), (int)r.n_rows);
   const int run = run_length(total);
   const int l = threadIdx.x % kLanes, group = threadIdx.x / kLanes;
   const int n_vec = 2 * a.Hkv;

@@ -1,7 +1,7 @@
 """The target's paged K/V cache beside a decode step (include/dspark_kv.h).
 
 PagedKV owns one layer's pages, the sequences' page table and lengths, and the
-workspaces of its calls, so that a layer of the target's verify forward launches
+workspaces of its calls (one stream at a time), so that a layer of the target's verify forward launches
 only library kernels and captures into the step's CUDA graph:
 
     kv.append(q, k, v, rows, q_out)      # norms, rotation, cache write
@@ -115,7 +115,8 @@ class PagedKV:
 
     def advance(self, n_accepted):
         """The sequences grow by the accepted tokens and the one the verify
-        emitted before them (whose row the step computed)."""
+        emitted before them (whose row the step computed).  A slot that was idle
+        (verify_len = -1) stays as it is with n_accepted = -1."""
         self.cache_len.add_(n_accepted).add_(1)
 
     def flags(self, stream=None):

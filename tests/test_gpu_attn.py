@@ -321,3 +321,47 @@ def test_positions_past_the_limit_are_flagged():
     torch.cuda.synchronize()
     assert D.dspark_get_device_flags(ws) == D.FLAG_BAD_LENGTH
     check(p, out, ref[1:])
+
+
+def test_rows_formed_one_by_one_over_a_long_sequence():
+    """A NaN in V that the rows of a few requests see, 393216 positions before
+    their new tokens: such a row is formed by itself, a CTA's for seconds, and
+    its waits hold out.  (Every position before the new ones is in one page, so
+    that the weights of its keys count 1536 times.)"""
+    B, n, D_, reps = 300, 256, 128, 1536
+    page, poisoned = n, (40, 41, 42)
+    g = torch.Generator(device="cuda").manual_seed(26)
+    k = torch.randn(6, 1, page, D_, generator=g, device="cuda").to(BF)
+    v = torch.randn(6, 1, page, D_, generator=g, device="cuda").to(BF)
+    q = torch.randn(B * n, 1, D_, generator=g, device="cuda").to(BF)
+    k[1], v[1] = k[0], v[0]
+    v[1, 0, 77, 5] = float("nan")
+    table = torch.zeros(B, reps + 1, dtype=torch.int32, device="cuda")
+    table[poisoned[0]:poisoned[-1] + 1] = 1
+    last = 2 + torch.arange(B, device="cuda") % 4
+    table[:, reps] = last.int()
+    row_start = torch.arange(B, device="cuda") * n
+    same = lambda x: torch.full((B,), x, dtype=torch.int32, device="cuda")  # noqa: E731
+    out = torch.full((B * n, 1, D_), MARK, dtype=BF, device="cuda")
+    ws = D.workspace(D.dspark_attn_workspace_size(B, 1, 1, D_, n), "cuda")
+    D.dspark_attn_verify(q, k, v, row_start, same(n - 1), same(reps * page), table, out, ws, n)
+    torch.cuda.synchronize()
+    assert D.dspark_get_device_flags(ws) == 0
+    for b in (0, 39, *poisoned, 43, 150, B - 1):
+        got = out[b * n:(b + 1) * n, 0].double()
+        kk = torch.cat([k[0, 0], k[2 + b % 4, 0]]).double()
+        vv = torch.cat([v[0, 0], v[2 + b % 4, 0]]).double()
+        w = torch.exp(q[b * n:(b + 1) * n, 0].double() @ kk.T / D_ ** 0.5)
+        w[:, :page] *= reps
+        w[:, page:].tril_()
+        w /= w.sum(1, keepdim=True)
+        want, mass = w @ vv, w @ vv.abs()
+        # half a step of bf16 for the result and, in the tiled kernel, the
+        # weights; fp32: scores (128 products, below 8e-5), the weights' and the
+        # results' sums (256 + 1537 additions of half a step, 1.1e-4 each),
+        # together below 2^-9 of the weighted |V|
+        tol = 2.0 ** -8 * (want.abs() + mass) + 2.0 ** -9 * mass
+        if b in poisoned:
+            assert bool(torch.isnan(got[:, 5]).all())
+            got[:, 5] = want[:, 5]
+        assert bool(((got - want).abs() <= tol).all()), b
