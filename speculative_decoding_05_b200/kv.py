@@ -52,8 +52,9 @@ def rope_frequencies(rot_dim: int, theta: float = 1e4, scaling: str = "none", fa
         def index_of(turns):  # where a frequency turns that often over original_len
             return half * math.log(original_len / (2 * math.pi * turns)) / math.log(theta)
 
+        # (high may lie beyond the last frequency: the ramp then ends beyond it too)
         low = max(math.floor(index_of(beta_fast)), 0)
-        high = min(math.ceil(index_of(beta_slow)), half - 1)
+        high = min(math.ceil(index_of(beta_slow)), rot_dim - 1)
         ramp = ((i - low) / max(high - low, 1e-3)).clamp(0.0, 1.0)
         return f * (1.0 - ramp) + f / factor * ramp, 0.1 * math.log(factor) + 1.0
     raise ValueError(f"scaling: {scaling!r} is not one of none, linear, ntk, yarn")
