@@ -32,7 +32,7 @@ def rope_frequencies(rot_dim: int, theta: float = 1e4, scaling: str = "none", fa
              "yarn":   frequencies that turn more than beta_fast times over
                        original_len positions stay, those that turn less than
                        beta_slow times are divided by factor, linear between
-                       (over the index); rope_scale 0.1 ln(factor) + 1
+                       (over the index); rope_scale 0.1 ln(factor) + 1, at least 1
     """
     if rot_dim <= 0 or rot_dim % 2:
         raise ValueError(f"rot_dim: want a positive even number, got {rot_dim}")
@@ -56,7 +56,7 @@ def rope_frequencies(rot_dim: int, theta: float = 1e4, scaling: str = "none", fa
         low = max(math.floor(index_of(beta_fast)), 0)
         high = min(math.ceil(index_of(beta_slow)), rot_dim - 1)
         ramp = ((i - low) / max(high - low, 1e-3)).clamp(0.0, 1.0)
-        return f * (1.0 - ramp) + f / factor * ramp, 0.1 * math.log(factor) + 1.0
+        return f * (1.0 - ramp) + f / factor * ramp, 0.1 * math.log(max(factor, 1.0)) + 1.0
     raise ValueError(f"scaling: {scaling!r} is not one of none, linear, ntk, yarn")
 
 

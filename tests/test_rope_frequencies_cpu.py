@@ -84,6 +84,12 @@ def test_yarn_divides_no_pair_by_the_whole_factor_that_turns_often_enough():
     assert fast and all(abs(float(f[i]) * theta ** (2.0 * i / rot) - 1.0) < 1e-12 for i in fast[:-1])
 
 
+@pytest.mark.parametrize("factor", [0.25, 0.5, 1.0])
+def test_yarn_without_stretching_keeps_the_attention_factor(factor):
+    """The published attention factor is 1 unless positions are stretched."""
+    assert rope_frequencies(64, 1e4, "yarn", factor, 4096)[1] == 1.0
+
+
 @pytest.mark.parametrize("bad", [dict(rot_dim=0), dict(rot_dim=15), dict(rot_dim=-4),
                                  dict(rot_dim=64, scaling="cubic"),
                                  dict(rot_dim=64, scaling="yarn", factor=4.0)])
