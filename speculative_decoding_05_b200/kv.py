@@ -65,7 +65,8 @@ class PagedKV:
 
     dtype: the rows' type (bfloat16 or float16) or float8_e4m3fn (quantised, one
     scale for each token and head).  page_table [B, max_pages] int32 may be
-    shared between layers; by default sequence b owns pages b * max_pages ..
+    shared between layers; by default sequence b owns pages b * max_pages .., so
+    that n_pages (default B * max_pages) can not be less.
     """
 
     def __init__(self, B: int, Hq: int, Hkv: int, head_dim: int, max_pages: int,
@@ -75,6 +76,9 @@ class PagedKV:
         self.page_size, self.max_len = page_size, max_len
         dev = torch.device(device)
         n_pages = B * max_pages if n_pages is None else n_pages
+        if page_table is None and n_pages < B * max_pages:
+            raise ValueError(f"n_pages: {n_pages} pages do not hold {B} sequences of {max_pages}; "
+                             "fewer need a page_table")
         shape = (n_pages, Hkv, page_size, head_dim)
         self.k_cache = torch.zeros(shape, dtype=dtype, device=dev)
         self.v_cache = torch.zeros(shape, dtype=dtype, device=dev)

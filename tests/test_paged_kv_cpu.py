@@ -1,0 +1,31 @@
+"""PagedKV's own bookkeeping, on the CPU (no kernel runs)."""
+import pytest
+import torch
+
+from speculative_decoding_05_b200 import build
+from speculative_decoding_05_b200.kv import PagedKV
+
+
+@pytest.fixture(scope="module", autouse=True)
+def lib():
+    build.build()
+
+
+def make(**kw):
+    return PagedKV(**dict(dict(B=3, Hq=4, Hkv=2, head_dim=64, max_pages=4, page_size=16,
+                               device="cpu"), **kw))
+
+
+def test_default_table_names_pages_that_exist():
+    for n in (None, 12, 20):
+        kv = make(n_pages=n)
+        assert int(kv.page_table.max()) < kv.k_cache.shape[0] and kv.page_table.shape == (3, 4)
+    for n in (0, 1, 11):
+        with pytest.raises(ValueError, match="n_pages"):
+            make(n_pages=n)
+
+
+def test_a_table_of_ones_own_may_share_fewer_pages():
+    table = torch.zeros(3, 4, dtype=torch.int32)
+    kv = make(n_pages=5, page_table=table)
+    assert kv.page_table is table and kv.k_cache.shape[0] == 5
