@@ -30,6 +30,12 @@
  * what the rejected tokens left behind it is overwritten by the next append
  * and never read as long as it lies beyond the sequence.
  *
+ * Idle slots.  These calls skip a slot with verify_len = -1.  dspark_verify*
+ * takes lengths of [0, K] only (it flags a negative one and goes on with 0): give
+ * it max(verify_len, 0), so that an idle slot is a request without drafts, whose
+ * row row_start[b] must exist and may hold anything finite; ignore what it
+ * returns for the slot, and leave cache_len[b] as it is.
+ *
  * Cache.  k_cache and v_cache are [n_pages, Hkv, page_size, D]; position j of
  * request b is place j % page_size of page page_table[b, j / page_size]
  * (page_table [B, max_pages] int32; entries behind a sequence's last page are

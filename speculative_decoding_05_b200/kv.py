@@ -7,10 +7,12 @@ only library kernels and captures into the step's CUDA graph:
     kv.append(q, k, v, rows, q_out)      # norms, rotation, cache write
     kv.attend(q_out, rows, out)          # attention of the new rows
     ...                                  # the rest of the target, dspark_verify*
-    kv.advance(n_accepted)               # the accepted tokens and the emitted one
+    kv.advance(n_accepted, rows)         # the accepted tokens and the emitted one
 
 `rows` are the row markers of the verify: (row_start [B] int64, verify_len [B]
-int32), which dspark_confidence_prefix writes on the device.
+int32), which dspark_confidence_prefix writes on the device.  A slot without a
+request has verify_len = -1 here and 0 in dspark_verify* (include/dspark_kv.h,
+"Idle slots").
 """
 from __future__ import annotations
 
@@ -118,11 +120,17 @@ class PagedKV:
                          self.cache_len if start is None else start, self.page_table, k_out, v_out,
                          self.ws, k_scale=self.k_scale, v_scale=self.v_scale, stream=stream)
 
-    def advance(self, n_accepted):
+    def advance(self, n_accepted, rows=None):
         """The sequences grow by the accepted tokens and the one the verify
-        emitted before them (whose row the step computed).  A slot that was idle
-        (verify_len = -1) stays as it is with n_accepted = -1."""
-        self.cache_len.add_(n_accepted).add_(1)
+        emitted before them (whose row the step computed).  With the step's
+        `rows`, slots that were idle in it (verify_len < 0) stay as they are,
+        whatever n_accepted says of them: dspark_verify* knows no idle slots and
+        counts one as a request without drafts.  Without `rows` an idle slot
+        needs n_accepted = -1."""
+        if rows is None:
+            self.cache_len.add_(n_accepted).add_(1)
+        else:
+            self.cache_len.add_((n_accepted + 1) * (rows[1] >= 0))
 
     def flags(self, stream=None):
         return {"kv": D.dspark_get_device_flags(self.ws, stream),

@@ -29,3 +29,18 @@ def test_a_table_of_ones_own_may_share_fewer_pages():
     table = torch.zeros(3, 4, dtype=torch.int32)
     kv = make(n_pages=5, page_table=table)
     assert kv.page_table is table and kv.k_cache.shape[0] == 5
+
+
+def test_advance_leaves_idle_slots():
+    """What the verify returns for an idle slot (a request without drafts) does
+    not move it; the accepted tokens and the emitted one move the others."""
+    kv = make()
+    kv.cache_len.copy_(torch.tensor([5, 0, 9], dtype=torch.int32))
+    rows = (torch.zeros(3, dtype=torch.int64), torch.tensor([2, -1, 0], dtype=torch.int32))
+    at = kv.cache_len
+    for n in (0, 3, -1):
+        kv.advance(torch.tensor([1, n, 0], dtype=torch.int32), rows)
+    assert kv.cache_len is at and kv.cache_len.dtype == torch.int32
+    assert kv.cache_len.tolist() == [11, 0, 12]
+    kv.advance(torch.tensor([1, -1, 0], dtype=torch.int32))
+    assert kv.cache_len.tolist() == [13, 0, 13]
