@@ -94,6 +94,8 @@ class PagedKV:
         self.cache_len = torch.zeros(B, dtype=torch.int32, device=dev)
         self.ws = D.workspace(D.dspark_kv_workspace_size(), dev)
         self.ws_attn = D.workspace(D.dspark_attn_workspace_size(B, Hq, Hkv, head_dim, max_len), dev)
+        for ws in (self.ws, self.ws_attn):  # flags() may come before a call
+            ws[:256].zero_()
 
     def _markers(self, rows):
         row_start, verify_len = rows

@@ -25,6 +25,17 @@ def test_default_table_names_pages_that_exist():
             make(n_pages=n)
 
 
+def test_status_is_clean_before_the_first_call(monkeypatch):
+    """flags() of a cache that was only appended to must not read what its
+    attention workspace's memory held before."""
+    from speculative_decoding_05_b200 import dspark as D
+    monkeypatch.setattr(D, "workspace",
+                        lambda n, device: torch.full((n,), 0xFF, dtype=torch.uint8, device=device))
+    kv = make()
+    for ws in (kv.ws, kv.ws_attn):
+        assert not bool(ws[:16].any())
+
+
 def test_a_table_of_ones_own_may_share_fewer_pages():
     table = torch.zeros(3, 4, dtype=torch.int32)
     kv = make(n_pages=5, page_table=table)
