@@ -143,7 +143,9 @@ size_t dspark_attn_workspace_size(int B, int Hq, int Hkv, int D, int max_len);
  *   over max(0, i - window + 1) <= j <= i   (window = 0: over all j <= i)
  * Scores, softmax statistics and sums are fp32; the weights are rounded to 16
  * bits (the value rows' type; fp16 with an e4m3 cache) for the product with
- * V; out is rounded once.  Positions a row does not see never reach it: K and
+ * V; out is rounded once.  With an e4m3 cache q enters the scores as a sum of
+ * e4m3 parts: elements below 2^-9 (bf16; fp16: 2^-6) of the largest of their row
+ * and head are off by up to 2^-17 of it, all others exact.  Positions a row does not see never reach it: K and
  * V there may hold anything, infinities and NaN included.  A row whose result is
  * not finite is formed again by itself: right, but slow.  (Over more than 2^19
  * positions such rows may hold a step's CTA up for longer than its waits' limit

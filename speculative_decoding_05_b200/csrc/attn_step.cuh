@@ -24,12 +24,15 @@
 // at the maximum of the first tile.)
 //
 // e4m3 cache: S^T takes K's codes as they lie, by the 8-bit MMA, and Q as a sum
-// of two e4m3 parts (three for fp16): an item's Q, scaled by a power of two to a
+// of two e4m3 parts (three for fp16): a row of Q, scaled by a power of two to a
 // largest element in [128, 256), is rounded to e4m3 (4 significant bits), the
 // rest rounded again (4 more).  bf16 has 8 and fp16 11 bits, so the sum is exact
-// for elements down to 2^-9 (2^-6) of the largest; below that it is off by at
-// most 2^-17 of the largest, a score then by 2^-17 of what the item's scores can
-// come to, less than the weights' rounding.  K's scale is applied to the scores.
+// for elements down to 2^-9 (2^-6) of the row's largest; below that it is off by
+// at most 2^-17 of it, a score by 2^-17 sm_scale max|q| sum|k|.  Each row has a power
+// of its own, which goes to its scores with K's scale: with one for all rows of an
+// item a loud row took its neighbours' bits.  (That costs nothing at 32 rows and
+// 128 elements: 64 requests over 4096 keys 137 us, with one power 144; 10 % at 64
+// rows of 64: 252 for 227.)
 // V's codes are widened to fp16 (exact) by 4 warps, and P is fp16 with V's scale
 // on it: the reference is such that the product stays in fp16's range.
 //
@@ -110,7 +113,7 @@ struct StepSmem {
   alignas(1024) unsigned char in_k[C::kQ8 ? C::kRingK : 1][C::kQ8 ? C::kTileIn : 16];
   alignas(1024) unsigned char in_v[C::kQ8 ? C::kRingV : 1][C::kQ8 ? C::kTileIn : 16];
   alignas(16) float scale[C::kQ8 ? kStepScales : 1][2][kStepKeys];
-  float qs[2];                      // e4m3: power of two that was taken off Q
+  alignas(16) float qs[2][C::kQ8 ? N : 4];  // e4m3: power of two taken off each row of Q
   alignas(16) float neg_m[2][N], f[2][N], part[2][4][N];  // of each stream: -m, ..
   int low[N], bad[N];
   long long out[N];
@@ -395,50 +398,66 @@ __global__ void __launch_bounds__(step_threads<TC>(), 1)
                        i / kChunks < it.n_rows);
           cp_async_wait_all();
         } else {
-          // the largest element, then its e4m3 parts
-          float top = 0.0f;
-          bool odd = false;  // fmaxf passes over a NaN
-#pragma unroll 8
-          for (int i = lane; i < N * kChunks; i += 32) {
-            float y[8];
-            unpack8<T>(*reinterpret_cast<const uint4*>(source(i)), y);
+          // a row on four lanes, 8 rows a set; all loads of some sets before the
+          // first store (stores might alias them: each would wait for its load)
+          constexpr int kPer = kChunks / 4, kSets = N / 8 < 8 / kPer ? N / 8 : 8 / kPer;
+          static_assert(N % (8 * kSets) == 0, "whole sets");
+#pragma unroll 1
+          for (int r0 = lane / 4; r0 < N; r0 += 8 * kSets) {
+            uint4 v[kSets][kPer];
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-              top = fmaxf(top, fabsf(y[e]));
-              odd |= !isfinite(y[e]);
+            for (int s = 0; s < kSets; ++s) {
+#pragma unroll
+              for (int k = 0; k < kPer; ++k) {
+                v[s][k] = *reinterpret_cast<const uint4*>(
+                    source((r0 + 8 * s) * kChunks + 4 * k + lane % 4));
+                if (r0 + 8 * s >= it.n_rows) v[s][k] = make_uint4(0, 0, 0, 0);
+              }
+            }
+#pragma unroll
+            for (int s = 0; s < kSets; ++s) {
+              const int r = r0 + 8 * s;
+              // the row's largest element, as bits: sizes in their order,
+              // infinities and NaN above them
+              uint32_t top = 0;
+#pragma unroll
+              for (int k = 0; k < kPer; ++k) {
+                float y[8];
+                unpack8<T>(v[s][k], y);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) top = max(top, __float_as_uint(y[e]) & 0x7fffffffu);
+              }
+              top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+              top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+              const int up = min(134 - (int)(top >> 23), 120);  // top 2^up in [128, 256)
+              const float mul = __uint_as_float((uint32_t)(127 + up) << 23);
+#pragma unroll
+              for (int k = 0; k < kPer; ++k) {
+                float y[8];
+                unpack8<T>(v[s][k], y);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) y[e] *= mul;
+#pragma unroll
+                for (int pt = 0; pt < C::kQParts; ++pt) {
+                  const uint32_t lo = f32_to_e4m3x4(y[0], y[1], y[2], y[3]);
+                  const uint32_t hi = f32_to_e4m3x4(y[4], y[5], y[6], y[7]);
+                  *reinterpret_cast<uint2*>(sm.q[qb] + pt * N * D +
+                                            k8_offset<D>(r, 8 * (4 * k + lane % 4))) =
+                      make_uint2(lo, hi);
+                  float z[8];
+                  e4m3x4_to_f32(lo, z);
+                  e4m3x4_to_f32(hi, z + 4);
+#pragma unroll
+                  for (int e = 0; e < 8; ++e) y[e] -= z[e];
+                }
+              }
+              // a value that is not finite has no such parts: the row's results
+              // become not finite, and it is formed by itself
+              if (lane % 4 == 0)
+                sm.qs[qb][r] = top >= 0x7f800000u ? CUDART_NAN_F
+                                                  : __uint_as_float((uint32_t)(127 - up) << 23);
             }
           }
-          top = warp_max(top);
-          odd = __any_sync(0xffffffffu, odd);
-          int e2;
-          frexpf(odd ? 1.0f : top, &e2);
-          const int up = min(8 - e2, 120);  // top 2^up in [128, 256)
-          const float mul = ldexpf(1.0f, up);
-#pragma unroll 4
-          for (int i = lane; i < N * kChunks; i += 32) {
-            const int r = i / kChunks, c = i % kChunks;
-            uint4 v = *reinterpret_cast<const uint4*>(source(i));
-            if (r >= it.n_rows) v = make_uint4(0, 0, 0, 0);
-            float y[8];
-            unpack8<T>(v, y);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) y[e] *= mul;
-#pragma unroll
-            for (int pt = 0; pt < C::kQParts; ++pt) {
-              const uint32_t lo = f32_to_e4m3x4(y[0], y[1], y[2], y[3]);
-              const uint32_t hi = f32_to_e4m3x4(y[4], y[5], y[6], y[7]);
-              *reinterpret_cast<uint2*>(sm.q[qb] + pt * N * D + k8_offset<D>(r, 8 * c)) =
-                  make_uint2(lo, hi);
-              float z[8];
-              e4m3x4_to_f32(lo, z);
-              e4m3x4_to_f32(hi, z + 4);
-#pragma unroll
-              for (int e = 0; e < 8; ++e) y[e] -= z[e];
-            }
-          }
-          // a value that is not finite has no such parts: the item's results
-          // become not finite, and its rows are formed one by one
-          if (lane == 0) sm.qs[qb] = odd ? CUDART_NAN_F : ldexpf(1.0f, -up);
         }
         fence_proxy_async_smem();
         mbar_arrive(&sm.q_full[qb]);
@@ -721,7 +740,6 @@ __global__ void __launch_bounds__(step_threads<TC>(), 1)
         }
         wait(&sm.s_full[buf], phase);
         tc_fence_after();
-        if constexpr (kQ8) kf *= sm.qs[qb];
         const uint64_t kf2 = pair_of(kf, kf), vsv = pair_of(vs, vs);
         const uint32_t s_col = lane_base + buf * N + n0;
 
@@ -734,12 +752,15 @@ __global__ void __launch_bounds__(step_threads<TC>(), 1)
           for (int i = 0; i < kX; i += 4) {
             float4 m4 = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
             if (over) m4 = *reinterpret_cast<const float4*>(&sm.neg_m[stream][n0 + c + i]);
-            pair_to(fma2(pair_of(__uint_as_float(raw[i]), __uint_as_float(raw[i + 1])), kf2,
-                         pair_of(m4.x, m4.y)),
-                    x[i], x[i + 1]);
-            pair_to(fma2(pair_of(__uint_as_float(raw[i + 2]), __uint_as_float(raw[i + 3])), kf2,
-                         pair_of(m4.z, m4.w)),
-                    x[i + 2], x[i + 3]);
+            uint64_t s0 = pair_of(__uint_as_float(raw[i]), __uint_as_float(raw[i + 1]));
+            uint64_t s1 = pair_of(__uint_as_float(raw[i + 2]), __uint_as_float(raw[i + 3]));
+            if constexpr (kQ8) {
+              const float4 q4 = *reinterpret_cast<const float4*>(&sm.qs[qb][n0 + c + i]);
+              s0 = mul2(s0, pair_of(q4.x, q4.y));
+              s1 = mul2(s1, pair_of(q4.z, q4.w));
+            }
+            pair_to(fma2(s0, kf2, pair_of(m4.x, m4.y)), x[i], x[i + 1]);
+            pair_to(fma2(s1, kf2, pair_of(m4.z, m4.w)), x[i + 2], x[i + 3]);
           }
           if (masked) {
 #pragma unroll

@@ -42,6 +42,32 @@ def run(p, **kw):
 
 # ---- rows beside each other --------------------------------------------------
 
+@pytest.mark.parametrize("act,big", [(BF, 1e3), (BF, 1e5), (BF, 1e20), (HF, 1e3), (HF, 6e4)])
+@pytest.mark.parametrize("D_", [64, 128])
+@pytest.mark.parametrize("n", [3, 8, 40])
+def test_a_loud_row_leaves_its_neighbours_their_bits(act, big, D_, n):
+    """One large finite element in the queries of one token and head: every
+    other row holds to the bound of its own elements."""
+    p = Problem([n, 2], [300, 60], 8, 2, D_, act, E4, 64, seed=31)
+    loud = p.start[0] + n // 2
+    p.q[loud, 2, 5] = big
+    p.q[loud, 6, 7] = -big
+    out, ws = attend(p)
+    torch.cuda.synchronize()
+    assert D.dspark_get_device_flags(ws) == 0
+    assert bool(torch.isfinite(out[loud].float()).all())
+    hold(out, attention_rows(p), [(loud, 2), (loud, 6)])
+
+
+@pytest.mark.parametrize("act", [BF, HF])
+def test_rows_of_very_different_sizes(act):
+    """Rows scaled by powers of two from 2^-12 to 2^3, each to its own bound."""
+    p = Problem([16], [500], 8, 2, 128, act, E4, 32, seed=32)
+    r = torch.arange(16, device="cuda")
+    p.q[p.rows_of(0)] = (p.q[p.rows_of(0)].float() * torch.exp2(r - 12.0)[:, None, None]).to(act)
+    run(p)
+
+
 # ---- one key far above the others ----------------------------------------------
 
 # ---- scores that rise ------------------------------------------------------------
