@@ -99,6 +99,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
   constexpr int kOps = S::kOps;
   constexpr bool kHalf = std::is_same<T, __half>::value;
   constexpr float kHot = kHalf ? 14.0f : 64.0f;  // as in the step kernel
+  constexpr float kLift = kHalf ? kHalfLift : 0.0f;
   constexpr int kColO = 256;                     // TMEM: S (then P) twice, O twice
   extern __shared__ unsigned char smem_raw[];
   S& sm = *reinterpret_cast<S*>(smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u));
@@ -439,7 +440,8 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
             top = fmaxf(top, sm.part[p][half ^ 1][r]);
             const float old = -neg_m;
             const bool seen = j > 0 && k0 > low;  // has keys before this tile
-            const float now = seen ? fmaxf(old, top) : top == -CUDART_INF_F ? old : top;
+            const float to = top - kLift;
+            const float now = seen ? fmaxf(old, to) : top == -CUDART_INF_F ? old : to;
             const float f = seen && now != old ? ex2(old - now) : 1.0f;
             neg_m = -now;
             l *= f;

@@ -21,7 +21,9 @@
 // precision in floating point while scores stay within 2^+-kHot, and one vote a
 // tile finds the rare tile with a score outside, where m moves to the maximum
 // and O^T and L are rescaled.  (fp16 weights have a short range: there m starts
-// at the maximum of the first tile.)
+// kLift below the maximum of the first tile, which stands in the middle of the
+// range that is left above it: with the maximum at 1 keys 2^-25 below it were lost
+// as a whole, however many.)
 //
 // e4m3 cache: S^T takes K's codes as they lie, by the 8-bit MMA, and Q as a sum
 // of two e4m3 parts (three for fp16): a row of Q, scaled by a power of two to a
@@ -64,6 +66,10 @@ constexpr int kStepMma = kStepSoftmax + 3;         // warp
 constexpr int kStepWiden = kStepSoftmax + 4;       // first of 4 warps, e4m3 only
 constexpr int kStepItems = 4;
 constexpr int kStepScales = 4;
+// fp16 weights: the largest is 2^kHalfLift where the reference was moved, 2^kHot at
+// most.  Their sums then keep what lies 2^(25 + kHalfLift) below it; less room above
+// moves references more often.
+constexpr float kHalfLift = 8.0f;
 constexpr int kSmemLimit = 232448;                 // 227 KB a CTA
 
 template <typename TC>
@@ -171,6 +177,7 @@ __global__ void __launch_bounds__(step_threads<TC>(), 1)
   // weights far from their ends, 2^14 fp16 ones.  At the first keys of a row a
   // score as far below it does so too (fp16: always).
   constexpr float kHot = kHalfP ? 14.0f : 64.0f;
+  constexpr float kLift = kHalfP ? kHalfLift : 0.0f;  // where a moved reference puts the maximum
   extern __shared__ unsigned char smem_raw[];
   S& sm = *reinterpret_cast<S*>(smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u));
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -792,7 +799,8 @@ __global__ void __launch_bounds__(step_threads<TC>(), 1)
                                       fmaxf(sm.part[stream][2][n], sm.part[stream][3][n]));
               // whether an earlier tile of this stream has keys of the row
               const bool seen = j > 1 && k0 - kStepKeys > sm.low[n];
-              const float now = seen ? fmaxf(old, top) : top == -CUDART_INF_F ? old : top;
+              const float to = top - kLift;
+              const float now = seen ? fmaxf(old, to) : top == -CUDART_INF_F ? old : to;
               sm.f[stream][n] = seen && now != old ? ex2(old - now) : 1.0f;
               sm.neg_m[stream][n] = -now;
             }

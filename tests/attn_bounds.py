@@ -8,7 +8,7 @@ from tests.kv_reference import F64, half_step, quantise
 E4 = torch.float8_e4m3fn
 # fp16 weights keep 2^-25 (half their smallest step) against a largest weight of
 # at least 2^LIFT
-LIFT = 0
+LIFT = 8
 
 
 def put(p, name, b, lo, x):

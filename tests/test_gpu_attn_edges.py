@@ -70,6 +70,27 @@ def test_rows_of_very_different_sizes(act):
 
 # ---- one key far above the others ----------------------------------------------
 
+@pytest.mark.parametrize("act,cache", TYPES)
+@pytest.mark.parametrize("n", [2, 100])
+def test_many_light_keys_behind_a_heavy_first_one(act, cache, n):
+    """The first key has all but 2^-14 of the weight, 4000 others 2^-26 each;
+    they alone have values in the other channels."""
+    B, L, D_ = 24, 4096, 64
+    p = Problem([n] * B, [L - n] * B, 8, 8, D_, act, cache, 64, seed=33)
+    p.q.fill_(1.0)
+    g = torch.Generator(device="cuda").manual_seed(34)
+    for b in range(B):
+        k = -1.0 + 0.05 * torch.randn(L, 8, 1, generator=g, device="cuda").expand(L, 8, D_)
+        v = 128.0 + 64.0 * torch.rand(L, 8, D_, generator=g, device="cuda")
+        v[:, :, 0] = 0
+        k, v = k.clone(), v
+        k[0], v[0] = 1.25, 0.0
+        v[0, :, 0] = 128.0
+        put(p, "k", b, 0, k)
+        put(p, "v", b, 0, v)
+    run(p, sm_scale=0.125)
+
+
 # ---- scores that rise ------------------------------------------------------------
 
 @pytest.mark.parametrize("act,cache", TYPES)
