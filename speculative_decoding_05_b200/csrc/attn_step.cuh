@@ -738,7 +738,10 @@ __global__ void __launch_bounds__(step_threads<TC>(), 1)
           wait(&sm.scale_full[sc], (uint32_t)(tile / kStepScales) & 1u);
           kf *= sm.scale[sc][0][key];
           vs = sm.scale[sc][1][key];
-          vs2 = fmaxf(__log2f(vs), -60.0f);  // P carries the scale: its size counts
+          // P carries the scale: its size counts.  (Down to 2^-80: the weights
+          // themselves then stay below 2^94, and their sums over all positions in
+          // fp32's range.)
+          vs2 = fmaxf(__log2f(vs), -80.0f);
           consumed(kf + vs2);
           // a scale behind the sequence may be anything
           if (at >= it.past + it.n) vs = vs2 = 0.0f;

@@ -152,6 +152,15 @@ def test_window_with_rising_scores(act, cache):
 
 # ---- values and scales -------------------------------------------------------------
 
+@pytest.mark.parametrize("power", [-40, -60, -75, -90, 60])
+@pytest.mark.parametrize("n", [3, 50])
+def test_small_and_large_values_keep_their_bits(power, n):
+    """V as a whole tiny or huge (scales by 2^power): results are that much."""
+    p = Problem([n, 1], [700, 90], 8, 2, 128, BF, E4, 64, seed=41)
+    p.v_scale *= 2.0 ** power
+    run(p)
+
+
 @pytest.mark.parametrize("cache,act", [(HF, HF), (BF, BF), (E4, BF), (E4, HF)])
 @pytest.mark.parametrize("bad", [float("nan"), float("inf"), -float("inf")])
 @pytest.mark.parametrize("n", [4, 70])
