@@ -6,7 +6,6 @@
 #include <cstdint>
 #include <cstring>
 #include <mutex>
-#include <vector>
 
 #include "common.cuh"
 #include "kv_status.h"
@@ -735,14 +734,14 @@ int dspark_get_device_flags(const void* workspace, void* stream) {
   if (cudaStreamSynchronize(s) != cudaSuccess) return -1;
   unsigned n = 0, f = h[0];
   if (spread_status(h, &n)) {  // a word for each CTA of the call's first kernel
-    std::vector<unsigned> words(n);
+    unsigned words[kMaxStatusCtas];  // (nothing that could throw at a C entry)
     const unsigned* first = static_cast<const unsigned*>(workspace) + kSpreadHeadWords;
-    if (cudaMemcpyAsync(words.data(), first, n * sizeof(unsigned), cudaMemcpyDeviceToHost, s) !=
+    if (cudaMemcpyAsync(words, first, n * sizeof(unsigned), cudaMemcpyDeviceToHost, s) !=
             cudaSuccess ||
         cudaStreamSynchronize(s) != cudaSuccess)
       return -1;
     f = 0;
-    for (const unsigned w : words) f |= w;
+    for (unsigned i = 0; i < n; ++i) f |= words[i];
   }
   return (int)(f & 0x7fffffffu);  // -1 stays reserved for CUDA errors
 }

@@ -7,6 +7,7 @@
 
 #include "../../include/dspark_kv.h"
 #include "common.cuh"
+#include "kv_status.h"
 
 namespace dspark {
 
@@ -21,8 +22,7 @@ namespace dspark {
 // calls' flags leave it clear), the count, a tag.
 constexpr unsigned kSpreadBit = 0x80000000u;
 constexpr unsigned kSpreadTag = 0x6b76666cu;
-constexpr int kSpreadFirst = 4;          // words before the CTAs' words
-constexpr int kMaxStatusCtas = 2044;
+constexpr int kSpreadFirst = kSpreadHeadWords;  // words before the CTAs' words
 constexpr size_t kKvHeaderBytes = 8192;  // (4 + 2044) words
 static_assert((kSpreadFirst + kMaxStatusCtas) * 4 == kKvHeaderBytes, "status words");
 
