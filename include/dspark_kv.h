@@ -104,7 +104,7 @@ size_t dspark_kv_workspace_size(void);
  *          16, at most D; the markers row_start [B] int64, verify_len and
  *          cache_len [B] int32, page_table
  * Outputs  q_out [n_rows, Hq, D] (contiguous; may be q itself where q is
- *          contiguous), k_cache, v_cache, and with e4m3 k_scale, v_scale
+ *          contiguous, else over none of q, k, v), k_cache, v_cache, and with e4m3 k_scale, v_scale
  */
 dspark_status dspark_kv_append(
     const void *q, const void *k, const void *v, int64_t q_stride, int64_t k_stride,
@@ -155,7 +155,7 @@ size_t dspark_attn_workspace_size(int B, int Hq, int Hkv, int D, int max_len);
  *          max_len: an upper bound of verify_len + 1, at least 1 (K + 1 of a
  *          verify step, the longest chunk of a prompt); it chooses the
  *          kernel, and a longer request is a data error; sm_scale > 0
- * Outputs  out [n_rows, Hq, D] act_dtype, contiguous
+ * Outputs  out [n_rows, Hq, D] act_dtype, contiguous, not over q
  */
 dspark_status dspark_attn_verify(
     const void *q, int64_t q_stride, dspark_kv_dtype act_dtype, int64_t n_rows, int B, int Hq,

@@ -20,6 +20,16 @@ namespace {
 
 bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
+// Bytes from the first of n 16-bit rows, `stride` elements apart, to the end of the last.
+size_t rows_bytes(long long n, long long stride, long long width) {
+  return 2 * (size_t)((n - 1) * stride + width);
+}
+// Whether n bytes at a and m bytes at b meet.
+bool meet(const void* a, size_t n, const void* b, size_t m) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return x < y ? y - x < n : x - y < m;
+}
+
 dspark_status launched(cudaError_t e) {
   if (e == cudaSuccess) return DSPARK_OK;
   cudaGetLastError();  // a refused launch also leaves its code behind
@@ -326,6 +336,14 @@ dspark_status dspark_kv_append(
   if (!aligned(q, 16) || !aligned(k, 16) || !aligned(v, 16) || !aligned(q_out, 16) ||
       !aligned(q_norm, 16) || !aligned(k_norm, 16) || !aligned(inv_freq, 8))
     return DSPARK_ERR_INVALID_ARG;
+  // a block writes its query rows when others may still have to read theirs
+  const long long wq = (long long)Hq * D, wk = (long long)Hkv * D;
+  const size_t out_bytes = rows_bytes(n_rows, wq, wq);
+  const bool in_place = q_out == q && (q_stride == wq || n_rows == 1);
+  if ((!in_place && meet(q_out, out_bytes, q, rows_bytes(n_rows, q_stride, wq))) ||
+      meet(q_out, out_bytes, k, rows_bytes(n_rows, k_stride, wk)) ||
+      meet(q_out, out_bytes, v, rows_bytes(n_rows, v_stride, wk)))
+    return DSPARK_ERR_INVALID_ARG;
   LaunchAppend l;
   AppendArgs& a = l.a;
   a.rows = make_rows(c, (int)n_rows);
@@ -402,6 +420,10 @@ dspark_status dspark_attn_verify(
   if (B == 0 || n_rows == 0) return no_work(workspace, s);
   if ((st = check_pointers(c)) != DSPARK_OK) return st;
   if (!q || !out || !aligned(q, 16) || !aligned(out, 16)) return DSPARK_ERR_INVALID_ARG;
+  // a row whose result is not finite is formed again from its query
+  const long long width = (long long)Hq * D;
+  if (meet(q, rows_bytes(n_rows, q_stride, width), out, rows_bytes(n_rows, width, width)))
+    return DSPARK_ERR_INVALID_ARG;
   LaunchAttn l;
   AttnArgs& a = l.a;
   a.rows = make_rows(c, max_len);
