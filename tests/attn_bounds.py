@@ -29,10 +29,13 @@ def attention_rows(p, sm_scale=None, window=0):
     keys that are seen.
 
     For element d of a row with weights w_j and A = sum_j w_j |v_jd|:
-      weights rounded once: u_p A; fp16 ones also by 2^-25 each where the largest
-        weight (16-bit cache: w_j; e4m3: w_j with V's scale, times a code of at most
-        448, which makes it w_j max_d |v_jd|) is at least 2^LIFT:
-        L 2^(-25 - LIFT) times the largest of these products;
+      weights rounded once, p_j = w_j (1 + d_j), |d_j| <= u_p: the product is off by
+        u_p A; where their sum is formed from the rounded ones, o = sum p v / sum p
+        moves by sum_j w_j d_j (v_jd - o), at most u_p (A + |o|);
+      fp16 weights also by 2^-25 each where the largest (16-bit cache: w_j; e4m3: w_j
+        with V's scale, times a code of at most 448, which makes it w_j max_d |v_jd|)
+        is at least 2^LIFT: L 2^(-25 - LIFT) times the largest of these products, for
+        product and sum;
       sums in fp32 over L keys: L 2^-23 A;
       a score: D products in fp32, D 2^-23 S for S the largest sum of |q k| scale of
         the row, its factor and 2^x (2^-21 and 2^-22 S); weight and normaliser, so
@@ -66,11 +69,11 @@ def attention_rows(p, sm_scale=None, window=0):
             if p.cache == E4:
                 part = 2.0 ** -17 * sm_scale * q[:, h].abs().amax(1, keepdim=True) * kh.abs().sum(1)
                 eps = eps + 2 * torch.where(seen, part, 0).amax(1, keepdim=True)
-            t = A * eps
+            t = A * eps + u_p * o.abs()
             if p.cache != torch.bfloat16:
                 top = (w * vh.abs().amax(1)).amax(1, keepdim=True) if p.cache == E4 else \
                     w.amax(1, keepdim=True) * vh.abs().amax()
-                t = t + L * 2.0 ** (-25 - LIFT) * top
+                t = t + 2 * L * 2.0 ** (-25 - LIFT) * top
             out[:, h] = o
             tol[:, h] = t + u_o * (o.abs() + t) + (2.0 ** -25 if p.act == torch.float16 else 0)
         res.append((p.rows_of(b), out, tol))
