@@ -131,7 +131,9 @@ dspark_status dspark_kv_read(
     void *workspace, size_t ws_bytes, void *stream);
 
 /* Workspace bytes of dspark_attn_verify: the status, and the partial results
- * of rows whose keys are split over several CTAs. */
+ * of rows whose keys are split over several CTAs: 39 MB at D = 128, 20 at 64,
+ * whatever B, Hq, Hkv and max_len are.  Calls that follow one another on a stream
+ * (the layers of a step) may share one. */
 size_t dspark_attn_workspace_size(int B, int Hq, int Hkv, int D, int max_len);
 
 /*

@@ -7,7 +7,7 @@
 // (16 a clock and SM).  So both must run all the time: two row tiles of 128 in
 // turn, one's softmax while the other's products are formed,
 //   S_p [128 rows, 128 keys] = Q_p K^T
-//   P_p = 2^(S_p - m), 16 bits, back to TMEM over S_p
+//   P_p = 2^(S_p - m), 16 bits (V's type, as in the step kernel), back to TMEM over S_p
 //   O_p [128 rows, D]       += P_p V      P from TMEM, V as it lies (MN-major)
 // with the MMAs in the order S0 S1 | PV0 S0' PV1 S1' | ..  A thread owns one row
 // of 64 keys: with all 128 a tile's softmax was a chain so long that the products
@@ -17,8 +17,8 @@
 // hardly ever rescaled; their two warps meet once a tile, to vote on that and
 // because the weights of one lie over the scores of the other.
 //
-// Measured: 390 us for chunks of 2 x 2048 tokens behind 2000 to 6000, 890
-// TFLOP/s, 54 % of the measured matrix rate; a pair of tiles takes some 3600
+// Measured: 390 to 399 us (by the box) for chunks of 2 x 2048 tokens behind 2000 to
+// 6000, 875 to 890 TFLOP/s, 53 % of the measured matrix rate; a pair of tiles takes some 3600
 // clocks of the 2160, what remains is the chain scores - weights - product of each.
 //
 // Warps: 16 softmax (two groups a row tile, which also load its Q rows), one that

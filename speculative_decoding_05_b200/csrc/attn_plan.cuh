@@ -25,10 +25,13 @@
 namespace dspark {
 
 // What an item costs besides its key tiles, in key tiles: rows loaded,
-// results merged and stored.
+// results merged and stored.  Measured (us) at 1, 2 and 4: 64 requests x 9 tokens
+// 127, 121, 117; e4m3 serving step 330, 312, 304; fp16 decode of heads of 64 190,
+// 167, 162; chunk 400, 390, 384; one token over 131071 104.5, 105, 105.5.
 constexpr int kItemCost = 2;
-// Least cost of a CTA's piece.  Below it a further CTA saves less than the
-// join of its part costs.
+// Least cost of a CTA's piece: a further CTA also costs a part for the join.  At 1,
+// 2 and 4: one request's block of 17 tokens 31.6, 31.6, 29.8, one token over 512
+// 14.6, 14.6, 14.9; batches are the same.
 constexpr int kMinPiece = 2;
 
 struct AttnTiles {

@@ -11,6 +11,10 @@
 //                                       [128 keys][N rows] written by the threads
 //   L   [., N rows]      += 1 P^T       the weights' sums, alike in every lane
 //                                       (e4m3: summed by the threads)
+// P is rounded to V's 16 bits: the product takes both operands in one type, and
+// tf32, with no more bits than fp16, at half the rate.  A weight is off by 2^-8
+// (bf16) or 2^-11 of itself at most, a result by as much of sum_j w_j |v_j|.  L is
+// summed from the rounded weights (e4m3: from the unrounded).
 // Two pairs of warpgroups take the tiles in turn, each with O^T and L of its
 // own, joined at the item's end: a tile's softmax is a chain of some 2000 clocks
 // (scores out of TMEM, exponentials, weights to shared memory, hand-over to the
@@ -44,10 +48,14 @@
 // buffers reach.
 //
 // Measured (whole calls, of the measured copy bandwidth where that bounds): 16-bit
-// caches 70 to 78 % (64 to 256 requests of some thousand tokens, one of 128 k);
-// e4m3 with 32 rows 53 %: the issue slots (0.56 of them used, 24 warps of
-// different code that wait for instructions a tenth of the time) bound it, not
-// the stream.  One request's step 14 us (host 14), a block of 16 31 us.
+// caches 72 to 78 % (64 to 256 requests of some thousand tokens, one of 128 k);
+// e4m3 with 32 rows 53 %: with 16 rows 123 us, with 32 137 (64 requests over 4096
+// keys), against a floor of 85, so most of what it costs over the stream is a key
+// tile's, whatever the rows: 24 warps of different code use 0.56 of the issue slots
+// and wait for each other's hand-overs and for instructions.  fp16 heads of 64 with
+// one row a head: 167 us, where a form on warp-level matrix instructions took 148:
+// a tile is half the bytes there for the same chain of hand-overs.  One request's
+// step 14 us (host 14), a block of 16 31 us.
 #pragma once
 
 #include <type_traits>

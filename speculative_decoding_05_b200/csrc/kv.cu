@@ -249,8 +249,9 @@ struct LaunchAttn {
   // 146, 32 160; with 32 rows, N = 32 164, 64 272; 16 bits with 80 rows, N = 80 198,
   // the chunk kernel 247 (its 256 rows mostly empty); with 96, two tiles of 80 350,
   // the chunk kernel 252; with 256, 412 and 324.  An e4m3 cache goes by tiles of up to 64
-  // rows whatever the rows: its operand rings and widened V leave no room for the
-  // chunk kernel's.
+  // rows whatever the rows (64 rows 266, 128 479: two tiles read every key twice):
+  // beside its rings and widened V the chunk kernel's 256 rows of Q have no room,
+  // and the sums of its rows in the epilogue want a power of two, not 80.
   template <typename T, typename TC, int Dh>
   dspark_status run() {
     if constexpr (sizeof(TC) != 1)

@@ -69,6 +69,13 @@ class PagedKV:
     scale for each token and head).  page_table [B, max_pages] int32 may be
     shared between layers; by default sequence b owns pages b * max_pages .., so
     that n_pages (default B * max_pages) can not be less.
+
+    max_len: the longest run of new rows that attend takes; it chooses the kernel,
+    and a longer run is flagged and left out.  K + 1 for the steps of a decode; a
+    prompt's chunk wants a bound of its own (a step under a chunk's bound is right
+    but slower): dspark_attn_verify over the same tensors takes one.  append and
+    read have no such bound.  ws_attn (39 MB at 128 elements) may be another
+    layer's, where both run on one stream.
     """
 
     def __init__(self, B: int, Hq: int, Hkv: int, head_dim: int, max_pages: int,
