@@ -246,7 +246,8 @@ struct LaunchAttn {
   // smallest N that holds them, since the threads' work on a key goes with N.
   // Measured (us; D = 128 but for the first): one fp16 row a head (16 heads of 64), 128 requests, N = 16 169, 32
   // 180, 64 211.  64 requests over 4096 keys, 8 heads: e4m3 with 16 rows, N = 16
-  // 146, 32 160; with 32 rows, N = 32 164, 64 272; 16 bits with 80 rows, N = 80 198,
+  // 147, 32 158; with 32 rows, N = 32 163, 64 281 (behind the 16-bit runs; by themselves
+  // 124, 134, 137, 256); 16 bits with 80 rows, N = 80 198,
   // the chunk kernel 247 (its 256 rows mostly empty); with 96, two tiles of 80 350,
   // the chunk kernel 252; with 256, 412 and 324.  An e4m3 cache goes by tiles of up to 64
   // rows whatever the rows (64 rows 266, 128 479: two tiles read every key twice):
